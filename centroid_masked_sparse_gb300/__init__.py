@@ -26,7 +26,22 @@ __all__ = ["MaskedHead", "MtpError", "CapturedCalls", "MTP_FINISH_ARGMAX", "MTP_
            "mtp_read_device_error", "mtp_profile_events", "mtp_packed_embeddings_bytes", "mtp_pack_embeddings", "mtp_gather_plan", "mtp_force_gather", "mtp_wait_test", "GATHER_KINDS",
            "mtp_masked_topk_keys", "mtp_decode_keys", "combine_keys", "sharded_topk_tokens",
            "MTP_DEVERR_TOKEN_RANGE",
-           "MTP_DEVERR_OFFSETS", "MTP_DEVERR_TIMEOUT", "lib"]
+           "MTP_DEVERR_OFFSETS", "MTP_DEVERR_TIMEOUT", "lib",
+           # the operators around the head (lm_ops, loaded on first use: it needs torch)
+           "Q4Weight", "KvCache", "TokenLogprobs", "mtp_q4_quantize", "mtp_q4_matvec", "mtp_kv_append",
+           "mtp_kv_attention", "mtp_kv_attention_workspace_bytes", "mtp_token_logprobs",
+           "mtp_token_logprobs_backward", "token_logprobs", "MTP_TYPE_F32", "MTP_TYPE_BF16", "MTP_KV_INT8",
+           "MTP_KV_E4M3", "MTP_KV_WORKSPACE_ZEROED", "MTP_MAX_TOP", "MTP_DEVERR_PAGE"]
+
+
+def __getattr__(name):
+    if name in __all__ or name == "lm_ops":
+        import importlib
+        ops = importlib.import_module(".lm_ops", __name__)
+        globals().update({n: getattr(ops, n) for n in ops.__all__}, lm_ops=ops)
+        if name in globals():
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

@@ -1,4 +1,4 @@
-"""ctypes loader and signatures for ``libmtp_head.so`` (the C ABI of include/mtp_head.h).
+"""ctypes loader and signatures for ``libmtp_head.so`` (the C ABI of include/*.h).
 
 There is no fallback: if the library has not been built the import of the
 binding fails with a message saying how to build it.
@@ -23,7 +23,7 @@ MTP_MAX_BATCH = 1024
 
 KERNEL_IDS = {"projection": 0, "topk": 1, "gather_score": 2, "fill": 3, "dense": 4}
 
-# Every function declared in include/mtp_head.h, with its ctypes signature.
+# Every function declared in include/*.h, with its ctypes signature.
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
@@ -49,7 +49,55 @@ class MtpHeadDesc(ctypes.Structure):
     ]
 
 
+class MtpQ4Desc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("device", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("ld_codes", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("softcap", ctypes.c_float),
+    ]
+
+
+class MtpKvDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("device", ctypes.c_int32),
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class MtpKvBatch(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("tokens", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32),
+        ("table_width", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
+    ]
+
+
 _DP = ctypes.POINTER(MtpHeadDesc)
+_QP = ctypes.POINTER(MtpQ4Desc)
+_KP = ctypes.POINTER(MtpKvDesc)
+_SP = ctypes.POINTER(MtpKvBatch)
+_i64 = ctypes.c_int64
+_f32 = ctypes.c_float
 
 SIGNATURES = {
     "mtp_workspace_bytes": (_sz, [_DP, _i32]),
@@ -75,6 +123,13 @@ SIGNATURES = {
     "mtp_profile_events": (_i32, [_i32, _p, _p]),
     "mtp_force_gather": (_i32, [_i32]),
     "mtp_wait_test": (_i32, [ctypes.c_int64, _i32]),
+    "mtp_q4_matvec": (_i32, [_QP, _p, _i64, _i32, _p, _i32, _i64, _p]),
+    "mtp_q4_quantize": (_i32, [_p, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p, _p, _p]),
+    "mtp_kv_append": (_i32, [_KP, _SP, _p, _i64, _i64, _p, _i64, _i64, _p]),
+    "mtp_kv_attention_workspace_bytes": (_sz, [_KP, _SP, _i32, _i32]),
+    "mtp_kv_attention": (_i32, [_KP, _SP, _p, _i64, _i64, _i32, _i32, _i32, _f32, _p, _p, _p, _sz, _p]),
+    "mtp_token_logprobs": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _f32, _i32, _p, _p, _p, _p, _p, _p, _i32, _p]),
+    "mtp_token_logprobs_backward": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _f32, _p, _p, _p, _p, _p, _i64, _i32, _p]),
 }
 
 _lib = None

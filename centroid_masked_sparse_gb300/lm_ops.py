@@ -1,0 +1,311 @@
+"""The operators around the masked head: 4-bit products, attention over an 8-bit cache, token log probabilities.
+
+Thin Python face of the C ABI in include/mtp_lm_ops.h, in the manner of the package's head: each ``mtp_``
+function has the name of the C entry point that it calls, takes torch tensors, runs on the current stream (or
+``stream``), allocates the outputs that the caller did not pass, and raises ``MtpError`` on a non-OK status.
+
+    weight = Q4Weight.quantize(w, group=64)                    # once
+    logits = mtp_q4_matvec(weight, hidden)                     # [B, M] fp32
+    cache = KvCache.allocate(pages, 64, kv_heads, head_dim)
+    mtp_kv_append(cache, page_table, lengths, k, v)
+    out, lse = mtp_kv_attention(cache, page_table, lengths + 1, q)
+    scored = mtp_token_logprobs(logits, tokens, top=5)
+    logprob, entropy = token_logprobs(logits, tokens)          # the same, differentiable
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._lib import MtpKvBatch, MtpKvDesc, MtpQ4Desc, check, lib
+
+__all__ = ["Q4Weight", "KvCache", "TokenLogprobs", "mtp_q4_quantize", "mtp_q4_matvec", "mtp_kv_append",
+           "mtp_kv_attention", "mtp_kv_attention_workspace_bytes", "mtp_token_logprobs",
+           "mtp_token_logprobs_backward", "token_logprobs", "MTP_TYPE_F32", "MTP_TYPE_BF16", "MTP_KV_INT8",
+           "MTP_KV_E4M3", "MTP_KV_WORKSPACE_ZEROED", "MTP_MAX_TOP", "MTP_DEVERR_PAGE"]
+
+MTP_TYPE_F32, MTP_TYPE_BF16 = 0, 1
+MTP_KV_INT8, MTP_KV_E4M3 = 0, 1
+MTP_KV_WORKSPACE_ZEROED = 262144
+MTP_MAX_TOP = 32
+MTP_DEVERR_PAGE = 0x8
+
+_TYPES = {torch.float32: MTP_TYPE_F32, torch.bfloat16: MTP_TYPE_BF16}
+_FORMATS = {"int8": MTP_KV_INT8, "e4m3": MTP_KV_E4M3}
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _vector(t, dtype, n, device):
+    """A contiguous vector of n elements on the call's GPU, or None."""
+    assert t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.device == device)
+    return _ptr(t)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights
+# ---------------------------------------------------------------------------
+class Q4Weight:
+    """A matrix [M, K] of 4-bit weights: w[m, k] = (code - zero) * scale of its group of columns.
+
+    codes    uint8 [M, K / 2]: byte j holds column 2j in its low and 2j + 1 in its high four bits; unit inner
+             stride, rows a multiple of 16 bytes apart
+    scales   bf16 [M, K / group], group 32, 64 or 128
+    zeros    uint8 [M, K / group] or None (8 everywhere)
+    """
+
+    def __init__(self, codes, scales, zeros=None):
+        assert codes.dtype == torch.uint8 and codes.dim() == 2 and codes.stride(1) == 1
+        assert scales.dtype == torch.bfloat16 and scales.is_contiguous() and scales.device == codes.device
+        assert scales.dim() == 2 and scales.shape[0] == codes.shape[0]
+        assert zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
+                                 and zeros.device == codes.device)
+        self.codes, self.scales, self.zeros, self.device = codes, scales, zeros, codes.device
+        self.rows, self.cols = int(codes.shape[0]), 2 * int(codes.shape[1])
+        self.group = self.cols // max(1, int(scales.shape[1]))
+        assert self.group * int(scales.shape[1]) == self.cols, "scales do not divide the columns into groups"
+        self.desc = MtpQ4Desc(rows=self.rows, cols=self.cols, group=self.group, device=self.device.index or 0,
+                              codes=codes.data_ptr(), ld_codes=codes.stride(0), scales=scales.data_ptr(),
+                              zeros=_ptr(zeros), softcap=0.0)
+
+    @classmethod
+    def quantize(cls, w, group=64, zeros=False, stream=None):
+        """The 4-bit form of a bf16 matrix (mtp_q4_quantize), a one-time step."""
+        return mtp_q4_quantize(w, group, zeros, stream)
+
+
+def mtp_q4_quantize(w, group=64, zeros=False, stream=None) -> Q4Weight:
+    """A Q4Weight of the bf16 matrix w [M, K] (unit inner stride, finite values), with zero points if asked."""
+    assert w.dtype == torch.bfloat16 and w.dim() == 2 and w.stride(1) == 1
+    rows, cols = w.shape
+    codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(rows, max(1, cols // group), dtype=torch.bfloat16, device=w.device)
+    points = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zeros else None
+    check(lib().mtp_q4_quantize(w.data_ptr(), w.stride(0), rows, cols, group, w.device.index or 0, codes.data_ptr(),
+                                codes.stride(0), scales.data_ptr(), _ptr(points), _stream(stream, w.device)),
+          "mtp_q4_quantize")
+    return Q4Weight(codes, scales, points)
+
+
+def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, stream=None):
+    """[B, M]: softcap(x @ w.T) of x bf16 [B, K], in fp32 or rounded once to bf16 (out's type, or out_dtype)."""
+    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == weight.cols and x.stride(1) == 1
+    assert x.device == weight.device
+    batch = int(x.shape[0])
+    if out is None:
+        out = torch.empty(batch, weight.rows, dtype=out_dtype, device=weight.device)
+    assert out.shape == (batch, weight.rows) and out.stride(1) == 1 and out.device == weight.device
+    desc = weight.desc
+    if softcap != 0.0:
+        desc = MtpQ4Desc.from_buffer_copy(desc)
+        desc.softcap = softcap
+    check(lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), x.stride(0) if batch > 1 else max(x.stride(0), weight.cols),
+                              batch, out.data_ptr(), _TYPES[out.dtype],
+                              out.stride(0) if batch > 1 else max(out.stride(0), weight.rows), _stream(stream, weight.device)),
+          "mtp_q4_matvec")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit cache
+# ---------------------------------------------------------------------------
+class KvCache:
+    """A paged cache of keys and values in 8 bits, one scale per page and head for each of the two.
+
+    k_codes, v_codes    uint8 [pages, kv_heads, page_tokens, head_dim] contiguous
+    k_scales, v_scales  fp32 [pages, kv_heads] contiguous
+    format              "int8" or "e4m3"
+    """
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, format="int8"):
+        for t in (k_codes, v_codes):
+            assert t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and t.shape == k_codes.shape
+        for t in (k_scales, v_scales):
+            assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == k_codes.shape[:2]
+        assert len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) == 1
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.format, self.device = format, k_codes.device
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = (int(n) for n in k_codes.shape)
+        self.errors = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._ws = None
+        self.desc = MtpKvDesc(num_pages=self.pages, page_tokens=self.page_tokens, kv_heads=self.kv_heads,
+                              head_dim=self.head_dim, format=_FORMATS[format], device=self.device.index or 0,
+                              k_codes=k_codes.data_ptr(), v_codes=v_codes.data_ptr(), k_scales=k_scales.data_ptr(),
+                              v_scales=v_scales.data_ptr(), error_word=self.errors.data_ptr())
+
+    @classmethod
+    def allocate(cls, pages, page_tokens, kv_heads, head_dim, format="int8", device="cuda"):
+        """An empty cache (zeros)."""
+        def codes():
+            return torch.zeros(pages, kv_heads, page_tokens, head_dim, dtype=torch.uint8, device=device)
+
+        def scales():
+            return torch.zeros(pages, kv_heads, dtype=torch.float32, device=device)
+        return cls(codes(), codes(), scales(), scales(), format)
+
+    def workspace(self, need, stream=None):
+        """A cached attention workspace of at least `need` bytes, zeroed on the call's stream when it is made."""
+        if self._ws is None or self._ws.numel() < need:
+            with torch.cuda.stream(stream):
+                self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return self._ws
+
+    def read_errors(self):
+        """The MTP_DEVERR_* bits that the calls so far have set (waits for the GPU), and clears them."""
+        bits = int(self.errors.item())
+        self.errors.zero_()
+        return bits
+
+
+def _batch_desc(cache, page_table, lengths, starts, tokens, max_tokens):
+    batch = int(page_table.shape[0])
+    assert page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.device == cache.device
+    assert page_table.stride(1) == 1 or page_table.shape[1] == 1
+    if max_tokens is None:
+        assert starts is None, "ragged calls need the most tokens that one sequence brings"
+        max_tokens = max(1, tokens // max(1, batch))
+    width = int(page_table.shape[1])
+    return MtpKvBatch(batch=batch, tokens=tokens, max_tokens=max_tokens, table_width=width,
+                      page_table=page_table.data_ptr(), ld_table=page_table.stride(0) if batch > 1 else width,
+                      lengths=_vector(lengths, torch.int32, batch, cache.device),
+                      starts=_vector(starts, torch.int32, batch + 1, cache.device))
+
+
+def _tokens_ok(cache, t):
+    assert t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[2] == cache.head_dim and t.stride(2) == 1
+    assert t.device == cache.device
+    return t
+
+
+def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, stream=None) -> None:
+    """Write k and v (bf16 [tokens, kv_heads, head_dim]) behind the lengths[b] tokens that each sequence has.
+
+    page_table int32 [B, width], lengths int32 [B]; sequence b brings rows starts[b]..starts[b + 1] (int32
+    [B + 1]; at most max_new of them), or without starts an equal share of the rows."""
+    assert _tokens_ok(cache, k).shape == _tokens_ok(cache, v).shape and k.shape[1] == cache.kv_heads
+    seqs = _batch_desc(cache, page_table, lengths, starts, int(k.shape[0]), max_new)
+    check(lib().mtp_kv_append(ctypes.byref(cache.desc), ctypes.byref(seqs), k.data_ptr(), k.stride(0), k.stride(1),
+                              v.data_ptr(), v.stride(0), v.stride(1), _stream(stream, cache.device)), "mtp_kv_append")
+
+
+def mtp_kv_attention_workspace_bytes(cache, page_table, lengths, tokens, heads, starts=None, max_q=None, max_len=0) -> int:
+    seqs = _batch_desc(cache, page_table, lengths, starts, int(tokens), max_q)
+    return int(lib().mtp_kv_attention_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(seqs), int(heads), int(max_len)))
+
+
+def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max_len=0, window=0, scale=None, out=None,
+                     lse=None, workspace=None, stream=None):
+    """(out bf16 [tokens, heads, head_dim], lse fp32 [tokens, heads]): causal attention of q over the cache.
+
+    lengths are the tokens of each sequence in the cache, with the ones that q belongs to; starts and max_q as
+    in mtp_kv_append; max_len bounds the lengths (0: the table's width); window 0 sees everything; scale is
+    head_dim ** -0.5 unless given."""
+    tokens, heads = int(_tokens_ok(cache, q).shape[0]), int(q.shape[1])
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+    if lse is None:
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=cache.device)
+    assert out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous() and out.device == cache.device
+    seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_q)
+    desc, library = ctypes.byref(cache.desc), lib()
+    if workspace is None:
+        workspace = cache.workspace(library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len),
+                                    stream)
+    check(library.mtp_kv_attention(desc, ctypes.byref(seqs), q.data_ptr(), q.stride(0), q.stride(1), heads, max_len,
+                                   window, cache.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                   _vector(lse, torch.float32, tokens * heads, cache.device), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream, cache.device)),
+          "mtp_kv_attention")
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Token log probabilities
+# ---------------------------------------------------------------------------
+class TokenLogprobs(NamedTuple):
+    """What mtp_token_logprobs returns, per row: fp32 logprob, entropy and lse, int32 rank, and with top > 0 the
+    top_ids (int32) and top_logprobs (fp32) [rows, top]."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    rank: torch.Tensor
+    lse: torch.Tensor
+    top_ids: Optional[torch.Tensor]
+    top_logprobs: Optional[torch.Tensor]
+
+
+def _logits_ok(logits):
+    assert logits.dim() == 2 and logits.dtype in _TYPES
+    assert logits.stride(1) == 1 or logits.shape[1] == 1
+    return int(logits.shape[0]), int(logits.shape[1])
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+
+
+def mtp_token_logprobs(logits, tokens, top=0, temperature=1.0, out=None, stream=None) -> TokenLogprobs:
+    """Log probability and rank of tokens[r] (int32 [rows]; outside the vocabulary: no token) in logits[r], the
+    row's entropy and lse, and its `top` largest alternatives.  out: an earlier result to write into."""
+    rows, vocab = _logits_ok(logits)
+    device = logits.device
+    if out is None:
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=device)
+        out = TokenLogprobs(empty(rows), empty(rows), empty(rows, dtype=torch.int32), empty(rows),
+                            empty(rows, top, dtype=torch.int32) if top else None, empty(rows, top) if top else None)
+    f32, i32 = torch.float32, torch.int32
+    check(lib().mtp_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], _row_stride(logits), rows, vocab,
+                                   _vector(tokens, i32, rows, device), temperature, top,
+                                   _vector(out.logprob, f32, rows, device), _vector(out.entropy, f32, rows, device),
+                                   _vector(out.rank, i32, rows, device), _vector(out.lse, f32, rows, device),
+                                   _vector(out.top_ids, i32, rows * top, device),
+                                   _vector(out.top_logprobs, f32, rows * top, device), device.index or 0,
+                                   _stream(stream, device)), "mtp_token_logprobs")
+    return out
+
+
+def mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy=None, temperature=1.0, out=None,
+                                stream=None):
+    """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with respect to the logits, in their
+    type.  out may be the logits themselves."""
+    rows, vocab = _logits_ok(logits)
+    device, f32 = logits.device, torch.float32
+    if out is None:
+        out = torch.empty(rows, vocab, dtype=logits.dtype, device=device)
+    assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == device
+    assert out.stride(1) == 1 or vocab == 1
+    check(lib().mtp_token_logprobs_backward(
+        logits.data_ptr(), _TYPES[logits.dtype], _row_stride(logits), rows, vocab, _vector(tokens, torch.int32, rows, device),
+        temperature, _vector(lse, f32, rows, device), _vector(entropy, f32, rows, device),
+        _vector(grad_logprob, f32, rows, device), _vector(grad_entropy, f32, rows, device), out.data_ptr(), _row_stride(out),
+        device.index or 0, _stream(stream, device)), "mtp_token_logprobs_backward")
+    return out
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, temperature):
+        scored = mtp_token_logprobs(logits, tokens, temperature=temperature)
+        ctx.save_for_backward(logits, tokens, scored.lse, scored.entropy)
+        ctx.temperature = temperature
+        return scored.logprob, scored.entropy
+
+    @staticmethod
+    def backward(ctx, grad_logprob, grad_entropy):
+        logits, tokens, lse, entropy = ctx.saved_tensors
+        grad = mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob.contiguous(),
+                                           grad_entropy.contiguous(), ctx.temperature)
+        return grad, None, None
+
+
+def token_logprobs(logits, tokens, temperature=1.0):
+    """(logprob, entropy), fp32 [rows], differentiable with respect to the logits [rows, vocab] (fp32 or bf16)."""
+    return _TokenLogprobs.apply(logits, tokens, temperature)
