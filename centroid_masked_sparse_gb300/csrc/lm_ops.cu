@@ -98,7 +98,7 @@ mtp_status mtp_q4_matvec(const mtp_q4_desc *d, const void *x, int64_t ld_x, int3
     if (batch == 0) return MTP_OK;
     if (!d->codes || !d->scales || !x || !out) return MTP_ERR_NULL;
     if (d->ld_codes < d->cols / 2 || ld_x < d->cols || ld_out < d->rows) return MTP_ERR_SHAPE;
-    if (d->ld_codes % 16 != 0 || ld_x % 8 != 0 || !aligned(d->codes, 16) || !aligned(x, 16) || !aligned(d->scales, 2) ||
+    if (d->ld_codes % 16 != 0 || ld_x % 8 != 0 || !aligned(d->codes, 16) || !aligned(x, 16) || !aligned(d->scales, 16) || !aligned(d->zeros, 16) ||
         !aligned(out, out_type == MTP_TYPE_F32 ? 4 : 2))
         return MTP_ERR_ALIGN;
     DeviceScope dev(d->device);

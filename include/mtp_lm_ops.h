@@ -43,8 +43,8 @@ extern "C" {
  *   codes     uint8 [M, ld_codes]: byte j of a row holds column 2j in its low and
  *             column 2j + 1 in its high four bits; 16-byte aligned
  *   ld_codes  bytes between rows, >= K / 2 and a multiple of 16
- *   scales    bf16 [M, K / group] contiguous
- *   zeros     uint8 [M, K / group] contiguous (values 0..15; only the low four bits are
+ *   scales    bf16 [M, K / group] contiguous, 16-byte aligned
+ *   zeros     uint8 [M, K / group] contiguous, 16-byte aligned (only the low four bits are
  *             read), or NULL for 8 everywhere
  *   softcap   each product y becomes cap * tanh(y / cap); 0: none; negative or NaN:
  *             MTP_ERR_SHAPE */
