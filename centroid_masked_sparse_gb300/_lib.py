@@ -54,11 +54,9 @@ class MtpQ4Desc(ctypes.Structure):
         ("rows", ctypes.c_int32),
         ("cols", ctypes.c_int32),
         ("group", ctypes.c_int32),
+        ("zeros", ctypes.c_int32),
         ("device", ctypes.c_int32),
-        ("codes", ctypes.c_void_p),
-        ("ld_codes", ctypes.c_int64),
-        ("scales", ctypes.c_void_p),
-        ("zeros", ctypes.c_void_p),
+        ("packed", ctypes.c_void_p),
         ("softcap", ctypes.c_float),
     ]
 
@@ -124,6 +122,8 @@ SIGNATURES = {
     "mtp_force_gather": (_i32, [_i32]),
     "mtp_wait_test": (_i32, [ctypes.c_int64, _i32]),
     "mtp_q4_matvec": (_i32, [_QP, _p, _i64, _i32, _p, _i32, _i64, _p]),
+    "mtp_q4_packed_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "mtp_q4_pack": (_i32, [_QP, _p, _i64, _p, _p, _p, _sz, _p]),
     "mtp_q4_quantize": (_i32, [_p, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p, _p, _p]),
     "mtp_kv_append": (_i32, [_KP, _SP, _p, _i64, _i64, _p, _i64, _i64, _p]),
     "mtp_kv_attention_workspace_bytes": (_sz, [_KP, _SP, _i32, _i32]),

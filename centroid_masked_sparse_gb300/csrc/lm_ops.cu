@@ -86,6 +86,41 @@ mtp_status check_logits(int32_t type, int64_t ld, int32_t rows, int32_t vocab, f
 
 extern "C" {
 
+size_t mtp_q4_packed_bytes(int32_t rows, int32_t cols, int32_t group, int32_t zeros)
+{
+    if (check_q4(rows, cols, group, 0) != MTP_OK) return 0;
+    return q4_layout(rows, cols, group, zeros != 0).total;
+}
+
+mtp_status mtp_q4_pack(const mtp_q4_desc *d, const void *codes, int64_t ld_codes, const void *scales, const void *zeros,
+                       void *packed, size_t packed_bytes, void *stream)
+{
+    if (!d) return MTP_ERR_NULL;
+    mtp_status st = check_q4(d->rows, d->cols, d->group, d->device);
+    if (st != MTP_OK) return st;
+    if (!codes || !scales || (d->zeros != 0) != (zeros != nullptr) || !packed) return MTP_ERR_NULL;
+    const Q4Layout L = q4_layout(d->rows, d->cols, d->group, d->zeros != 0);
+    if (ld_codes < d->cols / 2 || packed_bytes < L.total) return MTP_ERR_SHAPE;
+    if (!aligned(scales, 2) || !aligned(packed, 256)) return MTP_ERR_ALIGN;
+    DeviceScope dev(d->device);
+    if (!dev.ok) return MTP_ERR_CUDA;
+    Q4PackParams p{};
+    p.codes = (const uint8_t *)codes;
+    p.ld_codes = ld_codes;
+    p.scales = (const uint16_t *)scales;
+    p.zeros = (const uint8_t *)zeros;
+    p.M = d->rows;
+    p.K = d->cols;
+    p.G = d->cols / d->group;
+    p.group = d->group;
+    p.tiles = (int)(((int64_t)d->rows + 15) / 16);
+    p.blocks = (d->cols + 63) / 64;
+    p.out_codes = (uint8_t *)packed;
+    p.out_scales = p.out_codes + L.scales;
+    p.out_zeros = p.out_codes + L.zeros;
+    return cuda_status(launch_q4_pack(p, (cudaStream_t)stream));
+}
+
 mtp_status mtp_q4_matvec(const mtp_q4_desc *d, const void *x, int64_t ld_x, int32_t batch, void *out, int32_t out_type,
                          int64_t ld_out, void *stream)
 {
@@ -96,18 +131,17 @@ mtp_status mtp_q4_matvec(const mtp_q4_desc *d, const void *x, int64_t ld_x, int3
     if (batch < 0 || !(d->softcap >= 0.f)) return MTP_ERR_SHAPE;
     if (batch > MTP_MAX_BATCH) return MTP_ERR_UNSUPPORTED;
     if (batch == 0) return MTP_OK;
-    if (!d->codes || !d->scales || !x || !out) return MTP_ERR_NULL;
-    if (d->ld_codes < d->cols / 2 || ld_x < d->cols || ld_out < d->rows) return MTP_ERR_SHAPE;
-    if (d->ld_codes % 16 != 0 || ld_x % 8 != 0 || !aligned(d->codes, 16) || !aligned(x, 16) || !aligned(d->scales, 16) || !aligned(d->zeros, 16) ||
-        !aligned(out, out_type == MTP_TYPE_F32 ? 4 : 2))
+    if (!d->packed || !x || !out) return MTP_ERR_NULL;
+    if (ld_x < d->cols || ld_out < d->rows) return MTP_ERR_SHAPE;
+    if (ld_x % 8 != 0 || !aligned(d->packed, 256) || !aligned(x, 16) || !aligned(out, out_type == MTP_TYPE_F32 ? 4 : 2))
         return MTP_ERR_ALIGN;
     DeviceScope dev(d->device);
     if (!dev.ok) return MTP_ERR_CUDA;
+    const Q4Layout L = q4_layout(d->rows, d->cols, d->group, d->zeros != 0);
     Q4Params p{};
-    p.codes = (const uint8_t *)d->codes;
-    p.ld_codes = d->ld_codes;
-    p.scales = (const uint16_t *)d->scales;
-    p.zeros = (const uint8_t *)d->zeros;
+    p.codes = (const uint8_t *)d->packed;
+    p.scales = p.codes + L.scales;
+    p.zeros = d->zeros ? p.codes + L.zeros : nullptr;
     p.x = (const uint16_t *)x;
     p.ld_x = ld_x;
     p.out = out;
@@ -116,6 +150,7 @@ mtp_status mtp_q4_matvec(const mtp_q4_desc *d, const void *x, int64_t ld_x, int3
     p.K = d->cols;
     p.group = d->group;
     p.G = d->cols / d->group;
+    p.blocks = (d->cols + 63) / 64;
     p.B = batch;
     p.bf16_out = out_type == MTP_TYPE_BF16;
     p.softcap = d->softcap;

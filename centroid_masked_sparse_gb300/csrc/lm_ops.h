@@ -11,18 +11,31 @@ namespace mtp {
 // 4-bit products (q4.cu)
 // ---------------------------------------------------------------------------
 struct Q4Params {
-    const uint8_t *codes;    // [M, ld_codes]
-    long long ld_codes;      // bytes
-    const uint16_t *scales;  // bf16 [M, G]
-    const uint8_t *zeros;    // [M, G] or null (8)
+    const uint8_t *codes;    // packed (include/mtp_lm_ops.h), as are scales and zeros
+    const uint8_t *scales;
+    const uint8_t *zeros;    // or null (8)
     const uint16_t *x;       // bf16 [B, ld_x]
     long long ld_x;
     void *out;               // [B, ld_out] fp32 or bf16
     long long ld_out;
     int M, K, G, group, B;
+    int blocks;              // of 64 columns
     int bf16_out;
     float softcap;
 };
+struct Q4PackParams {
+    const uint8_t *codes;    // [M, ld_codes]
+    long long ld_codes;      // bytes
+    const uint16_t *scales;  // bf16 [M, G]
+    const uint8_t *zeros;    // [M, G] or null
+    int M, K, G, group, tiles, blocks;
+    uint8_t *out_codes, *out_scales, *out_zeros;
+};
+struct Q4Layout {            // byte offsets of the packed form's parts
+    size_t scales, zeros, total;
+};
+Q4Layout q4_layout(int M, int K, int group, bool zeros);
+cudaError_t launch_q4_pack(const Q4PackParams &p, cudaStream_t s);
 cudaError_t launch_q4_matvec(const Q4Params &p, cudaStream_t s);
 cudaError_t launch_q4_quantize(const uint16_t *w, long long ld_w, int M, int K, int group, uint8_t *codes,
                                long long ld_codes, uint16_t *scales, uint8_t *zeros, cudaStream_t s);

@@ -1,5 +1,7 @@
 // Products with 4-bit weights (their kernel: q4_kernel.cuh), and the rounding of a bf16
 // matrix to that form.
+#include <algorithm>
+
 #include "lm_ops.h"
 
 namespace mtp {
@@ -51,7 +53,59 @@ k_q4_quantize(const uint16_t *w, long long ld_w, long long groups, int G, int gr
     }
 }
 
+// One thread per four bytes of the packed codes, then per (row, group) of scales and zero points.
+__global__ void __launch_bounds__(256) k_q4_pack(Q4PackParams p)
+{
+    const long long words = (long long)p.tiles * p.blocks * 128, step = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step) {
+        const int j = (int)(i % 4), lane = (int)(i / 4 % 32);
+        const long long block = i / 128, tile = block / p.blocks;
+        const long long row = tile * 16 + lane / 4 + j % 2 * 8;
+        const int byte = (int)(block % p.blocks) * 32 + j / 2 * 16 + lane % 4 * 4;
+        uint32_t v = 0;
+        if (row < p.M && byte < p.K / 2)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) v |= (uint32_t)p.codes[row * p.ld_codes + byte + b] << (8 * b);
+        ((uint32_t *)p.out_codes)[i] = v;
+    }
+    const int sg = 256 / p.group, steps = (p.K + 255) / 256;
+    const long long groups = (long long)p.tiles * steps * 8 * sg;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < groups; i += step) {
+        const int j = (int)(i % sg), g = (int)(i / sg % 8);
+        const long long ts = i / sg / 8, tile = ts / steps;
+        const long long at = ts % steps * sg + j;
+        uint32_t s = 0, z = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long row = tile * 16 + g + h * 8;
+            if (row >= p.M || at >= p.G) continue;
+            s |= (uint32_t)p.scales[row * p.G + at] << (16 * h);
+            if (p.zeros) z |= (uint32_t)(p.zeros[row * p.G + at] & 15) << (8 * h);
+        }
+        ((uint32_t *)p.out_scales)[i] = s;
+        if (p.zeros) ((uint16_t *)p.out_zeros)[i] = (uint16_t)z;
+    }
+}
+
 }  // namespace
+
+Q4Layout q4_layout(int M, int K, int group, bool zeros)
+{
+    Q4Layout L{};
+    const size_t tiles = ((size_t)M + 15) / 16, groups = tiles * ((K + 255) / 256) * 8 * (256 / group);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    L.scales = up(tiles * ((K + 63) / 64) * 512);
+    L.zeros = L.scales + up(groups * 4);
+    L.total = L.zeros + (zeros ? up(groups * 2) : 0);
+    return L;
+}
+
+cudaError_t launch_q4_pack(const Q4PackParams &p, cudaStream_t s)
+{
+    const long long words = (long long)p.tiles * p.blocks * 128;
+    k_q4_pack<<<(unsigned)std::min((words + 255) / 256, 32ll * sm_count()), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
 
 template <int GROUP> cudaError_t launch_q4_group(const Q4Params &p, cudaStream_t s);   // q4_kernel.cuh
 

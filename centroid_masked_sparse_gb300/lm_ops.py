@@ -54,45 +54,50 @@ def _vector(t, dtype, n, device):
 # 4-bit weights
 # ---------------------------------------------------------------------------
 class Q4Weight:
-    """A matrix [M, K] of 4-bit weights: w[m, k] = (code - zero) * scale of its group of columns.
+    """A matrix [M, K] of 4-bit weights, w[m, k] = (code - zero) * scale of its group of columns, packed for
+    mtp_q4_matvec when it is made (the tensors that it is made from need not be kept).
 
     codes    uint8 [M, K / 2]: byte j holds column 2j in its low and 2j + 1 in its high four bits; unit inner
-             stride, rows a multiple of 16 bytes apart
+             stride
     scales   bf16 [M, K / group], group 32, 64 or 128
     zeros    uint8 [M, K / group] or None (8 everywhere)
     """
 
-    def __init__(self, codes, scales, zeros=None):
+    def __init__(self, codes, scales, zeros=None, stream=None):
         assert codes.dtype == torch.uint8 and codes.dim() == 2 and codes.stride(1) == 1
         assert scales.dtype == torch.bfloat16 and scales.is_contiguous() and scales.device == codes.device
         assert scales.dim() == 2 and scales.shape[0] == codes.shape[0]
         assert zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
                                  and zeros.device == codes.device)
-        self.codes, self.scales, self.zeros, self.device = codes, scales, zeros, codes.device
+        self.device = codes.device
         self.rows, self.cols = int(codes.shape[0]), 2 * int(codes.shape[1])
         self.group = self.cols // max(1, int(scales.shape[1]))
         assert self.group * int(scales.shape[1]) == self.cols, "scales do not divide the columns into groups"
-        self.desc = MtpQ4Desc(rows=self.rows, cols=self.cols, group=self.group, device=self.device.index or 0,
-                              codes=codes.data_ptr(), ld_codes=codes.stride(0), scales=scales.data_ptr(),
-                              zeros=_ptr(zeros), softcap=0.0)
+        size = lib().mtp_q4_packed_bytes(self.rows, self.cols, self.group, zeros is not None)
+        self.packed = torch.empty(size, dtype=torch.uint8, device=self.device)
+        self.desc = MtpQ4Desc(rows=self.rows, cols=self.cols, group=self.group, zeros=zeros is not None,
+                              device=self.device.index or 0, packed=self.packed.data_ptr(), softcap=0.0)
+        check(lib().mtp_q4_pack(ctypes.byref(self.desc), codes.data_ptr(), codes.stride(0) if self.rows > 1 else self.cols // 2,
+                                scales.data_ptr(), _ptr(zeros), self.packed.data_ptr(), size, _stream(stream, self.device)),
+              "mtp_q4_pack")
 
     @classmethod
     def quantize(cls, w, group=64, zeros=False, stream=None):
         """The 4-bit form of a bf16 matrix (mtp_q4_quantize), a one-time step."""
-        return mtp_q4_quantize(w, group, zeros, stream)
+        return cls(*mtp_q4_quantize(w, group, zeros, stream), stream=stream)
 
 
-def mtp_q4_quantize(w, group=64, zeros=False, stream=None) -> Q4Weight:
-    """A Q4Weight of the bf16 matrix w [M, K] (unit inner stride, finite values), with zero points if asked."""
+def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
+    """(codes, scales, zeros or None) of the bf16 matrix w [M, K] (unit inner stride, finite values)."""
     assert w.dtype == torch.bfloat16 and w.dim() == 2 and w.stride(1) == 1
     rows, cols = w.shape
     codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(rows, max(1, cols // group), dtype=torch.bfloat16, device=w.device)
     points = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zeros else None
-    check(lib().mtp_q4_quantize(w.data_ptr(), w.stride(0), rows, cols, group, w.device.index or 0, codes.data_ptr(),
-                                codes.stride(0), scales.data_ptr(), _ptr(points), _stream(stream, w.device)),
-          "mtp_q4_quantize")
-    return Q4Weight(codes, scales, points)
+    check(lib().mtp_q4_quantize(w.data_ptr(), w.stride(0) if rows > 1 else cols, rows, cols, group, w.device.index or 0,
+                                codes.data_ptr(), max(1, cols // 2), scales.data_ptr(), _ptr(points),
+                                _stream(stream, w.device)), "mtp_q4_quantize")
+    return codes, scales, points
 
 
 def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, stream=None):

@@ -35,17 +35,13 @@ extern "C" {
 
 /* A matrix of `rows` x `cols` weights in 4 bits, with one scale (and optionally one
  * zero point) for each group of `group` consecutive columns of a row:
- *   w[m, k] = (code[m, k] - z) * scale[m, k / group],   z = zeros[m, k / group] or 8.
+ *   w[m, k] = (code[m, k] - z) * scale[m, k / group],   z = zero[m, k / group] or 8.
  *   rows      M >= 1
  *   cols      K, a multiple of group, 32 <= K <= MTP_Q4_MAX_COLS
  *   group     32, 64 or 128
+ *   zeros     whether there are zero points (0: 8 everywhere)
  *   device    CUDA ordinal of every buffer
- *   codes     uint8 [M, ld_codes]: byte j of a row holds column 2j in its low and
- *             column 2j + 1 in its high four bits; 16-byte aligned
- *   ld_codes  bytes between rows, >= K / 2 and a multiple of 16
- *   scales    bf16 [M, K / group] contiguous, 16-byte aligned
- *   zeros     uint8 [M, K / group] contiguous, 16-byte aligned (only the low four bits are
- *             read), or NULL for 8 everywhere
+ *   packed    the matrix as mtp_q4_pack lays it out, 256-byte aligned
  *   softcap   each product y becomes cap * tanh(y / cap); 0: none; negative or NaN:
  *             MTP_ERR_SHAPE */
 #define MTP_Q4_MAX_COLS 16384
@@ -53,26 +49,47 @@ typedef struct mtp_q4_desc {
     int32_t rows;
     int32_t cols;
     int32_t group;
+    int32_t zeros;
     int32_t device;
-    const void *codes;
-    int64_t ld_codes;
-    const void *scales;
-    const void *zeros;
+    const void *packed;
     float softcap;
 } mtp_q4_desc;
+
+/* The packed matrix: mtp_q4_pack lays codes, scales and zero points out once, like loading
+ * the weights, in the order in which mtp_q4_matvec's warps read them; what it was packed
+ * from need not be kept.  Rows go in tiles of 16, columns in blocks of 64 (codes) and steps
+ * of 256 (scales), with T = ceil(M / 16), B = ceil(K / 64), S = ceil(K / 256),
+ * n = 256 / group, and each part padded to 256 bytes:
+ *   codes    uint32 [T][B][32 lanes][4]: of lane 4g + t, word j holds row g + (j % 2) * 8 of
+ *            the tile and columns 64 b + (j / 2) * 32 + 8t .. + 7, the lowest four bits first
+ *   scales   bf16 [T][S][8][n][2]: of row g (then g + 8) and group s * n + i
+ *   zeros    uint8 of the same shape (only if there are any)
+ * with zeros in place of what the matrix does not have.  mtp_q4_packed_bytes: the size, or
+ * 0 for invalid sizes.
+ *   codes     uint8 [M, ld_codes]: byte j of a row holds column 2j in its low and
+ *             column 2j + 1 in its high four bits; ld_codes >= K / 2 bytes
+ *   scales    bf16 [M, K / group] contiguous
+ *   zeros     uint8 [M, K / group] contiguous (only the low four bits are read); not NULL
+ *             exactly if desc->zeros
+ * desc->packed and softcap are not read. */
+MTP_API size_t mtp_q4_packed_bytes(int32_t rows, int32_t cols, int32_t group, int32_t zeros);
+MTP_API mtp_status mtp_q4_pack(const mtp_q4_desc *desc, const void *codes, int64_t ld_codes, const void *scales,
+                               const void *zeros, void *packed, size_t packed_bytes, void *stream);
 
 /* out[b, m] = softcap(sum_k w[m, k] * x[b, k]).
  *   x         bf16 [batch, ld_x], 16-byte aligned, ld_x >= K and a multiple of 8
  *   out       [batch, ld_out] of out_type (MTP_TYPE_F32, or MTP_TYPE_BF16: rounded once,
  *             to nearest even), aligned to its element, ld_out >= M
- *   batch     0..MTP_MAX_BATCH; each 32 rows (fewer for long columns) read the codes once
- * Codes, x and zero points enter the products exactly; sums, scales and the softcap are
- * fp32.  Non-finite x or scales give what IEEE arithmetic gives in their outputs only. */
+ *   batch     0..MTP_MAX_BATCH; each 32 rows read the codes once
+ * Codes and zero points enter the products exactly, x to 2^-35 of its row's largest value
+ * or better (all of its 8 bits, unless it is below 2^-25 of that); sums, scales and the
+ * softcap are fp32.  A row of x that holds a NaN or an infinity gives NaN; non-finite scales
+ * give what IEEE arithmetic gives in their outputs only. */
 MTP_API mtp_status mtp_q4_matvec(const mtp_q4_desc *desc, const void *x, int64_t ld_x, int32_t batch,
                                  void *out, int32_t out_type, int64_t ld_out, void *stream);
 
 /* Round a bf16 matrix w [rows, ld_w] (finite values) to codes, scales and zero points in
- * the layout above; a one-time step.  Per group, in fp32 with IEEE division:
+ * the layout that mtp_q4_pack reads; a one-time step.  Per group, in fp32 with IEEE division:
  *   zeros == NULL   scale = bf16(max|w| / 7), code = clamp(rint(w / scale) + 8, 0, 15)
  *   otherwise       lo = min(0, min w), hi = max(0, max w), scale = bf16((hi - lo) / 15),
  *                   zero = clamp(rint(-lo / scale), 0, 15),

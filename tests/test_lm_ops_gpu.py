@@ -87,7 +87,7 @@ def test_q4_strides_and_padding():
     """Rows of codes, x and outputs further apart than their width; what lies between is neither read nor written."""
     g = gen(6)
     codes, scales, points = q4_weight(g, 100, 320, 64, True)
-    wide = torch.full((100, 256), 255, dtype=torch.uint8, device=DEV)
+    wide = torch.full((100, 257), 255, dtype=torch.uint8, device=DEV)
     wide[:, :160] = codes
     x = torch.full((11, 512), math.nan, dtype=BF16, device=DEV)
     x[:, :320] = randn(g, 11, 320).to(BF16)
@@ -115,11 +115,48 @@ def test_q4_extremes():
     close(mtp.mtp_q4_matvec(w, x).cpu()[fits], want[fits], (tol + 1e-38)[fits])
     x[4, 7] = math.nan
     scales[9, 1] = math.nan
-    got = mtp.mtp_q4_matvec(w, x).cpu()
+    got = mtp.mtp_q4_matvec(mtp.Q4Weight(codes, scales), x).cpu()
     assert torch.isnan(got[4]).all() and torch.isnan(got[:, 9]).all()
     keep = fits.clone()
     keep[4], keep[:, 9] = False, False
     close(got[keep], want[keep], (tol + 1e-38)[keep])
+
+
+def test_q4_packed_layout():
+    """The packed form, word by word as it is specified."""
+    g = gen(10)
+    for rows, cols, group in ((37, 352, 32), (16, 64, 64), (5, 640, 128)):
+        codes, scales, points = (t.cpu() for t in q4_weight(g, rows, cols, group, True))
+        packed = mtp.Q4Weight(*(t.to(DEV) for t in (codes, scales, points))).packed.cpu()
+        tiles, blocks, steps, n = -(-rows // 16), -(-cols // 64), -(-cols // 256), 256 // group
+        full = torch.zeros(tiles * 16, blocks * 32, dtype=torch.uint8)
+        full[:rows, :cols // 2] = codes
+        # [tile][half of 8 rows][g][block][half of 32 columns][t][4 bytes]
+        want = full.view(tiles, 2, 8, blocks, 2, 4, 4).permute(0, 3, 2, 5, 4, 1, 6).reshape(-1)
+        at = -(-want.numel() // 256) * 256
+        assert torch.equal(packed[:want.numel()], want)
+        for part in (scales.view(torch.uint8).view(rows, -1, 2), points[..., None]):
+            full = torch.zeros(tiles * 16, steps * n, part.shape[-1], dtype=torch.uint8)
+            full[:rows, :cols // group] = part
+            want = full.view(tiles, 2, 8, steps, n, -1).permute(0, 3, 2, 4, 1, 5).reshape(-1)
+            assert torch.equal(packed[at:at + want.numel()], want)
+            at += -(-want.numel() // 256) * 256
+        assert at == packed.numel()
+
+
+def test_q4_rows_of_x_far_apart():
+    """Each row of x has its own range: a large value beside small ones loses none of their bits down to 2^-25."""
+    g = gen(26)
+    codes, scales, points = q4_weight(g, 80, 512, 64, True)
+    x = randn(g, 9, 512).to(BF16)
+    x[:, 1::7] *= 2.0 ** -22
+    x[3] *= 2.0 ** 100
+    x[4] *= 2.0 ** -100
+    x[5] = 0.0
+    x[6] = 0.0
+    x[6, 100] = 2.0 ** -130   # subnormal
+    want, tol = ref.q4_matvec(codes, scales, points, 64, x, 0.0, False)
+    close(mtp.mtp_q4_matvec(mtp.Q4Weight(codes, scales, points), x), want, tol + 2e-45)
 
 
 def test_q4_beyond_32_bits():
@@ -144,12 +181,15 @@ def test_q4_quantize(rows, cols, group, zeros):
     w[0, :group] = 0.0
     if rows > 2:
         w[2] = w[2].abs()   # no value below zero
-    got = mtp.Q4Weight.quantize(w, group, zeros)
+    got = mtp.mtp_q4_quantize(w, group, zeros)
     codes, scales, points = ref.q4_quantize(w.contiguous(), group, zeros)
-    assert torch.equal(got.scales.cpu(), scales) and torch.equal(got.codes.cpu(), codes)
-    assert (got.zeros is None) == (points is None)
+    assert torch.equal(got[1].cpu(), scales) and torch.equal(got[0].cpu(), codes)
+    assert (got[2] is None) == (points is None)
     if zeros:
-        assert torch.equal(got.zeros.cpu(), points)
+        assert torch.equal(got[2].cpu(), points)
+    x = randn(g, 2, cols).to(BF16)
+    want, tol = ref.q4_matvec(codes, scales, points, group, x, 0.0, False)
+    close(mtp.mtp_q4_matvec(mtp.Q4Weight.quantize(w, group, zeros), x), want, tol)
 
 
 # ---------------------------------------------------------------------------

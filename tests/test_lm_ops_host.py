@@ -16,16 +16,16 @@ def L():
 
 def q4(**kw):
     from centroid_masked_sparse_gb300._lib import MtpQ4Desc
-    return MtpQ4Desc(**{**dict(rows=100, cols=256, group=64, device=0, codes=0x1000, ld_codes=128, scales=0x2000, zeros=None,
-                               softcap=0.0), **kw})
+    return MtpQ4Desc(**{**dict(rows=100, cols=256, group=64, zeros=0, device=0, packed=0x1000, softcap=0.0), **kw})
 
 
-@pytest.mark.parametrize("desc,call,expect", [
-    (dict(rows=0), {}, SHAPE), (dict(cols=0), {}, SHAPE), (dict(cols=250), {}, SHAPE), (dict(group=16), {}, UNSUPPORTED),
-    (dict(group=128, cols=192), {}, SHAPE), (dict(cols=16384 + 64, ld_codes=16384), {}, UNSUPPORTED),
-    (dict(device=-1), {}, SHAPE), (dict(codes=None), {}, NULL), (dict(scales=None), {}, NULL),
-    (dict(codes=0x1008), {}, ALIGN), (dict(ld_codes=136), {}, ALIGN), (dict(ld_codes=112), {}, SHAPE),
-    (dict(scales=0x2001), {}, ALIGN), (dict(softcap=-1.0), {}, SHAPE), (dict(softcap=float("nan")), {}, SHAPE),
+Q4_REFUSALS = [(dict(rows=0), {}, SHAPE), (dict(cols=0), {}, SHAPE), (dict(cols=250), {}, SHAPE), (dict(group=16), {}, UNSUPPORTED),
+               (dict(group=128, cols=192), {}, SHAPE), (dict(cols=16384 + 64), {}, UNSUPPORTED), (dict(device=-1), {}, SHAPE)]
+
+
+@pytest.mark.parametrize("desc,call,expect", Q4_REFUSALS + [
+    (dict(packed=None), {}, NULL), (dict(packed=0x1080), {}, ALIGN),
+    (dict(softcap=-1.0), {}, SHAPE), (dict(softcap=float("nan")), {}, SHAPE),
     ({}, dict(x=None), NULL), ({}, dict(out=None), NULL), ({}, dict(x=0x3004), ALIGN), ({}, dict(ld_x=255), SHAPE),
     ({}, dict(ld_x=260), ALIGN), ({}, dict(ld_out=99), SHAPE), ({}, dict(out=0x4002), ALIGN), ({}, dict(batch=-1), SHAPE),
     ({}, dict(batch=1025), UNSUPPORTED), ({}, dict(out_type=2), UNSUPPORTED), ({}, dict(batch=0, x=None, out=None), 0),
@@ -34,6 +34,24 @@ def test_q4_matvec_refuses(L, desc, call, expect):
     c = {**dict(x=0x3000, ld_x=256, batch=4, out=0x4000, out_type=0, ld_out=100), **call}
     assert L.mtp_q4_matvec(ctypes.byref(q4(**desc)), c["x"], c["ld_x"], c["batch"], c["out"], c["out_type"], c["ld_out"],
                            None) == expect
+
+
+@pytest.mark.parametrize("desc,call,expect", Q4_REFUSALS + [
+    ({}, dict(codes=None), NULL), ({}, dict(scales=None), NULL), ({}, dict(packed=None), NULL), ({}, dict(zeros=0x7000), NULL),
+    (dict(zeros=1), {}, NULL), ({}, dict(ld=127), SHAPE), ({}, dict(size=1000), SHAPE), ({}, dict(scales=0x3001), ALIGN),
+    ({}, dict(packed=0x4010), ALIGN),
+])
+def test_q4_pack_refuses(L, desc, call, expect):
+    c = {**dict(codes=0x2001, ld=128, scales=0x3000, zeros=None, packed=0x4000, size=1 << 30), **call}
+    assert L.mtp_q4_pack(ctypes.byref(q4(**desc)), c["codes"], c["ld"], c["scales"], c["zeros"], c["packed"], c["size"],
+                         None) == expect
+
+
+def test_q4_packed_bytes(L):
+    # 7 tiles of 16 rows: 4 blocks of 512 bytes, 1 step of 8 x 4 x 2 scales of 2 bytes
+    assert L.mtp_q4_packed_bytes(100, 256, 64, 0) == 7 * 4 * 512 + (7 * 128 + 255) // 256 * 256
+    assert L.mtp_q4_packed_bytes(100, 256, 64, 1) == L.mtp_q4_packed_bytes(100, 256, 64, 0) + (7 * 64 + 255) // 256 * 256
+    assert L.mtp_q4_packed_bytes(100, 250, 64, 0) == 0 and L.mtp_q4_packed_bytes(0, 256, 64, 0) == 0
 
 
 def test_q4_matvec_refuses_no_descriptor(L):
