@@ -11,16 +11,16 @@
 //    row's largest value to [2^14, 2^15): exact down to 2^-29 of that value (columns that
 //    meet bits 4-7 are also divided by 16: 2^-25), with an absolute error below 2^-39
 //    (2^-35) of it beneath;
-//  - the zero point leaves the sum through its start: -z * sum_k x[b, k] of the group, in
-//    fp32.  Its magnitude is about that of the sum (codes lie in 0..15), so the difference
-//    loses about one bit of fp32's 24.
-// The group's sum times its scale is then added to the row's sum in fp32.
+//  - the zero point leaves the sum as -z * sum_k x[b, k] of the group, in fp32.  Its
+//    magnitude is about that of the sum (codes lie in 0..15), so the difference loses about
+//    one bit of fp32's 24.
+// Both, times the group's scale, are added to the row's sum in fp32.
 //
-// What bounds it.  HBM for batches up to 16: 4.25 bits a weight with groups of 64.  The
-// tensor pipe takes 8 cycles per 1024 weights and 8 batch rows (measured), HBM 21, so
-// from 24 rows on the products bound it.  The integer pipe, the next one, takes 10 per 1024
-// weights; unpacking to bf16 with a subtraction of the zero point took 23 and that kernel
-// 61 us for 262144 x 1536 in groups of 64 and 8 rows.
+// What bounds it.  HBM up to 8 batch rows: 4.25 bits a weight with groups of 64; 262144 x
+// 1536 with 8 rows takes 43 us, 5.1 TB/s, the same loads and stores without the products
+// 41.7.  Above, the products: the tensor pipe takes 8 cycles for each mma and is 46 % busy
+// at 16 rows (56 us), 88 us at 32.  Unpacking to bf16 with a subtraction of the zero point
+// took 23 integer instructions for every 8 here (and that kernel 61 us at 8 rows).
 #pragma once
 
 #include <algorithm>
@@ -36,13 +36,16 @@ namespace {
 struct Q4Plan {
     int tiles;      // tiles of 16 rows in all
     int parts;      // warps that share a row's columns
-    int chunk;      // columns of x in shared memory at a time, a multiple of kCols or >= K
+    int chunk;      // columns of x in shared memory at a time, a multiple of kCols
 };
 
 constexpr int kTiles = 2;    // row tiles of a warp that share one read of x
 constexpr int kCols = 256;   // columns of a step: 4 blocks of 64
-constexpr int kSlots = 2;    // of a warp's ring
-constexpr int kStage = kTiles * 2048;
+
+// Bytes of a tile's scales and zero points in a step, and of a ring slot.
+template <int GROUP> constexpr int kScales = 8 * (kCols / GROUP) * 4;
+template <int GROUP> constexpr int kZeros = kScales<GROUP> / 2;
+template <int GROUP, bool ZEROS> constexpr int kStage = kTiles * (2048 + kScales<GROUP> + (ZEROS ? kZeros<GROUP> : 0));
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
@@ -56,6 +59,21 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Byte b of v (below 16) as a float: or-ed into 2^23, whose last place is 1.
+template <int B> __device__ __forceinline__ float byte_value(uint32_t v)
+{
+    return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7650 + B)) - 8388608.f;
 }
 
 // acc += s * d on a pair, with one instruction.
@@ -74,21 +92,22 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi)
     return r;
 }
 
-// NT: batch rows / 8; GROUP: columns of a group; ZEROS: zero points; W: warps.
-template <int NT, int GROUP, bool ZEROS, int W>
+// NT: batch rows / 8; GROUP: columns of a group; ZEROS: zero points; W: warps; S: slots of a
+// warp's ring.
+template <int NT, int GROUP, bool ZEROS, int W, int S>
 __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan)
 {
     constexpr int WORDS = GROUP / 32;      // words of a lane in a group
     constexpr int SG = kCols / GROUP;      // groups of a step
+    constexpr int STAGE = kStage<GROUP, ZEROS>, SCALES = kScales<GROUP>, ZPS = kZeros<GROUP>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_factor[NT * 8], s_inverse[NT * 8];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int b0 = blockIdx.y * NT * 8;
-    uint8_t *ring = smem + warp * kSlots * kStage + lane * 16;
-    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
-    uint4 *xs = (uint4 *)(smem + W * kSlots * kStage);                    // [word][NT][lane]
-    const int chunk = min(plan.chunk, p.K);
-    float *xw = (float *)(xs + chunk / 32 * NT * 32);                     // [word][NT * 8] sums of 32 columns
+    const uint8_t *ring = smem + warp * S * STAGE;
+    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+    uint4 *xs = (uint4 *)(smem + W * S * STAGE);                          // [word][NT][lane, see below]
+    float *xw = (float *)(xs + plan.chunk / 32 * NT * 32);                   // [word][NT * 8] sums of 32 columns
     const int blocks = p.blocks, all_steps = (p.K + kCols - 1) / kCols;
 
     // tiles of this CTA, then of this warp.  Its work is a list of rounds (kTiles tiles each),
@@ -106,9 +125,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         *hi = first + n * (part + 1) / plan.parts;
     };
 
-    // loads run ahead of the products through the same list, codes into the ring, scales
-    // (and zero points) of rows g and g + 8 for the step's groups into registers
-    uint32_t n_sc[kTiles][SG], n_zp[kTiles][SG / 2];
+    // loads run ahead of the products through the same list
     int l_tile = t_lo, l_chunk = 0, l_k, l_hi;
     share(0, &l_k, &l_hi);
     auto load = [&](int slot) {
@@ -118,41 +135,41 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         }
         if (l_tile >= t_hi) return;
         const int n = min(blocks - l_k * 4, 4);
+        const uint32_t dst = ring_s + slot * STAGE;
 #pragma unroll
         for (int r = 0; r < kTiles; ++r) {
             if (l_tile + r >= t_hi) break;
             const uint8_t *src = p.codes + ((long long)(l_tile + r) * blocks + l_k * 4) * 512 + lane * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < n) cp_async16(ring_s + slot * kStage + r * 2048 + i * 512, src + i * 512);
-            const long long at = ((long long)(l_tile + r) * all_steps + l_k) * 8 + g;
-            if (SG == 2) {
-                const uint2 v = __ldg((const uint2 *)p.scales + at);
-                n_sc[r][0] = v.x, n_sc[r][1] = v.y;
-            } else {
-#pragma unroll
-                for (int j = 0; j < SG; j += 4) {
-                    const uint4 v = __ldg((const uint4 *)p.scales + at * (SG / 4) + j / 4);
-                    n_sc[r][j % SG] = v.x, n_sc[r][(j + 1) % SG] = v.y, n_sc[r][(j + 2) % SG] = v.z, n_sc[r][(j + 3) % SG] = v.w;
-                }
-            }
-            if (ZEROS)
-#pragma unroll
-                for (int j = 0; j < SG / 2; ++j) n_zp[r][j] = __ldg((const uint32_t *)p.zeros + at * (SG / 2) + j);
+                if (i < n) cp_async16(dst + r * 2048 + i * 512, src + i * 512);
+            const long long at = (long long)(l_tile + r) * all_steps + l_k;
+            if (lane < SCALES / 16) cp_async16(dst + kTiles * 2048 + r * SCALES, p.scales + at * SCALES + lane * 16);
+            if (ZEROS && lane < ZPS / 16)
+                cp_async16(dst + kTiles * (2048 + SCALES) + r * ZPS, p.zeros + at * ZPS + lane * 16);
         }
         ++l_k;
     };
-    load(0);
-    cp_async_commit();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        load(i);
+        cp_async_commit();
+    }
 
-    // each batch row's power of two
+    // A warp takes batch rows warp, warp + W, ..., eight loads of a lane in flight: first each
+    // row's largest value and its power of two ...
     for (int n = warp; n < NT * 8; n += W) {
         uint32_t top = 0;
-        if (b0 + n < p.B)
-            for (int k = lane * 8; k < p.K; k += 256) {
-                const uint4 v = ld_ro16(p.x + (b0 + n) * p.ld_x + k);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-            }
+        const uint16_t *x = p.x + (b0 + n) * p.ld_x;
+        for (int k = lane * 8; k < p.K && b0 + n < p.B; k += 2048) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = k + i * 256 < p.K ? ld_ro16(x + k + i * 256) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                             __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        }
         top = max(top >> 16, top & 0xffffu);
         top = __reduce_max_sync(~0u, top);
         if (lane == 0) {
@@ -162,7 +179,40 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
             s_inverse[n] = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float(e == 254u ? 0x00400000u : (254u - e) << 23);
         }
     }
-    __syncthreads();
+    __syncwarp();
+    // ... then x of a chunk in the operand's order: the 16 bytes of lane (g, t) lie at lane
+    // (g ^ (word % 8), t), which spreads a row's words over the banks.  Beside it the sums of
+    // a group's columns, in the place of its first word.
+    auto stage_x = [&](int c) {
+        const int k0 = c * plan.chunk, words = min(plan.chunk, all_steps * kCols - k0) / 32;
+        for (int n = warp; n < NT * 8; n += W) {
+            const uint16_t *x = p.x + (b0 + n) * p.ld_x + k0;
+            const int left = b0 + n < p.B ? p.K - k0 : 0;
+            const float f = s_factor[n];
+            uint4 *dst = xs + n / 8 * 32 + ((n % 8 ^ g) * 4 + t);   // of word i * 8 + g
+            for (int w0 = 0; w0 < words; w0 += 64) {
+                uint4 u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = (w0 + i * 8) * 32 + lane * 8;
+                    u[i] = k < left ? ld_ro16(x + k) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int word = w0 + i * 8 + g;
+                    if (w0 + i * 8 >= words) break;   // words is a multiple of 8
+                    const float v0 = bf_lo(u[i].x) * f, v1 = bf_hi(u[i].x) * f, v2 = bf_lo(u[i].y) * f, v3 = bf_hi(u[i].y) * f;
+                    const float v4 = bf_lo(u[i].z) * f, v5 = bf_hi(u[i].z) * f, v6 = bf_lo(u[i].w) * f, v7 = bf_hi(u[i].w) * f;
+                    dst[word * NT * 32] = make_uint4(half_pair(v0, v4), half_pair(v1 * 0.0625f, v5 * 0.0625f), half_pair(v2, v6),
+                                                     half_pair(v3 * 0.0625f, v7 * 0.0625f));
+                    float sum = ((v0 + v4) + (v1 + v5)) + ((v2 + v6) + (v3 + v7));
+#pragma unroll
+                    for (int o = 1; o < 4 * WORDS; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+                    if (lane % (4 * WORDS) == 0) xw[word * NT * 8 + n] = sum * ((ZEROS ? -1.f : -8.f) / 16777216.f);
+                }
+            }
+        }
+    };
 
     float acc[kTiles][NT][4];
 #pragma unroll
@@ -185,98 +235,72 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         const int tile = t_lo + round * kTiles, live = min(t_hi - tile, kTiles);
         for (int c = 0; c < chunks; ++c) {
             if (chunks > 1 || round == 0) {
-                // x of the chunk in the operand's order; its sums by 32 columns, then by group
-                const int k0 = c * plan.chunk, words = min(chunk, p.K - k0) / 32;
                 if (chunks > 1) __syncthreads();
-                for (int i = threadIdx.x; i < words * NT * 32; i += W * 32) {
-                    const int n = i / 32 % NT * 8 + lane / 4;
-                    float v[8] = {};
-                    if (b0 + n < p.B) {
-                        const uint4 u = ld_ro16(p.x + (b0 + n) * p.ld_x + k0 + i / (32 * NT) * 32 + t * 8);
-                        const float f = s_factor[n];
-                        v[0] = bf_lo(u.x) * f, v[1] = bf_hi(u.x) * f, v[2] = bf_lo(u.y) * f, v[3] = bf_hi(u.y) * f;
-                        v[4] = bf_lo(u.z) * f, v[5] = bf_hi(u.z) * f, v[6] = bf_lo(u.w) * f, v[7] = bf_hi(u.w) * f;
-                    }
-                    xs[i] = make_uint4(half_pair(v[0], v[4]), half_pair(v[1] * 0.0625f, v[5] * 0.0625f), half_pair(v[2], v[6]),
-                                       half_pair(v[3] * 0.0625f, v[7] * 0.0625f));
-                    float sum = ((v[0] + v[4]) + (v[1] + v[5])) + ((v[2] + v[6]) + (v[3] + v[7]));
-                    sum += __shfl_xor_sync(~0u, sum, 1);
-                    sum += __shfl_xor_sync(~0u, sum, 2);
-                    if (t == 0) xw[i / 32 * 8 + g] = sum * ((ZEROS ? -1.f : -8.f) / 16777216.f);
-                }
+                stage_x(c);
                 __syncthreads();
-                if (WORDS > 1) {   // the first word's place takes the group's sum
-                    for (int i = threadIdx.x; i < words / WORDS * NT * 8; i += W * 32) {
-                        float *at = xw + i / (NT * 8) * (WORDS * NT * 8) + i % (NT * 8);
-                        float sum = at[0];
-#pragma unroll
-                        for (int w = 1; w < WORDS; ++w) sum += at[w * NT * 8];
-                        at[0] = sum;
-                    }
-                    __syncthreads();
-                }
             }
             int k, k_hi;
             share(c, &k, &k_hi);
             if (live <= 0) k = k_hi;
             for (; k < k_hi; ++k) {
-                cp_async_wait<0>();   // a lane reads only what it copied itself
-                uint32_t sc[kTiles][SG], zp[kTiles][SG / 2];
-#pragma unroll
-                for (int r = 0; r < kTiles; ++r) {
-#pragma unroll
-                    for (int j = 0; j < SG; ++j) sc[r][j] = n_sc[r][j];
-#pragma unroll
-                    for (int j = 0; j < SG / 2; ++j) zp[r][j] = n_zp[r][j];
-                }
-                load(slot ^ 1);
+                cp_async_wait<S - 2>();
+                __syncwarp();   // the step is there for every lane, and the slot of the one before is free
+                load(slot == 0 ? S - 1 : slot - 1);
                 cp_async_commit();
-                const uint8_t *codes = ring + slot * kStage;
-                slot ^= 1;
+                const uint8_t *codes = ring + slot * STAGE + lane * 16;
+                const uint8_t *scales = ring + slot * STAGE + kTiles * 2048 + g * SG * 4;
+                const uint8_t *zeros = ring + slot * STAGE + kTiles * (2048 + SCALES) + g * SG * 2;
+                slot = slot == S - 1 ? 0 : slot + 1;
                 const int word0 = k * (kCols / 32) - c * (plan.chunk / 32);
+                const uint4 *xk = xs + word0 * NT * 32;
+                const float *sk = xw + word0 * NT * 8 + t * 2;
+                // No branch in here: a tile that is not there and columns beyond K are computed
+                // too, the one on whatever the slot holds (and not stored), the others on
+                // zeros of x with scales of zero.
 #pragma unroll
                 for (int j = 0; j < SG; ++j) {
-                    if (k * SG + j >= p.G) break;
-                    uint4 x[WORDS][NT];
+                    float d[kTiles][NT][4];
+#pragma unroll
+                    for (int w = j * WORDS; w < (j + 1) * WORDS; ++w) {
+                        uint4 x[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) x[n] = xk[(w * NT + n) * 32 + ((g ^ w) * 4 + t)];
+#pragma unroll
+                        for (int r = 0; r < kTiles; ++r) {
+                            // words of rows g and g + 8: a block holds two words of each
+                            const uint4 block = *(const uint4 *)(codes + r * 2048 + w / 2 * 512);
+                            const uint32_t lo = w % 2 ? block.z : block.x, hi = w % 2 ? block.w : block.y;
+                            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                if (w == j * WORDS)
+                                    mma_f16_first(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
+                                else
+                                    mma_f16(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(d[r][n], lo8 & 0x000f000fu, hi8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x00f000f0u, x[n].z, x[n].w);
+                        }
+                    }
                     float2 sum[NT];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sum[n] = *(const float2 *)(xw + ((word0 + j * WORDS) * NT + n) * 8 + t * 2);
-#pragma unroll
-                        for (int w = 0; w < WORDS; ++w) x[w][n] = xs[((word0 + j * WORDS + w) * NT + n) * 32 + lane];
-                    }
+                    for (int n = 0; n < NT; ++n) sum[n] = *(const float2 *)(sk + (j * WORDS * NT + n) * 8);
 #pragma unroll
                     for (int r = 0; r < kTiles; ++r) {
-                        if (r >= live) break;
-                        const float s_lo = bf_lo(sc[r][j]), s_hi = bf_hi(sc[r][j]);
-                        float d[NT][4];
+                        const uint32_t s2 = *(const uint32_t *)(scales + r * SCALES + j * 4);
+                        const float s_lo = bf_lo(s2), s_hi = bf_hi(s2);
+                        float z_lo = s_lo, z_hi = s_hi;   // 8 is in the sums of x
                         if (ZEROS) {
-                            const uint32_t z = zp[r][j / 2] >> (j % 2 * 16);
-                            const float z_lo = (float)(z & 15u), z_hi = (float)(z >> 8 & 15u);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                d[n][0] = z_lo * sum[n].x, d[n][1] = z_lo * sum[n].y, d[n][2] = z_hi * sum[n].x, d[n][3] = z_hi * sum[n].y;
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) d[n][0] = d[n][2] = sum[n].x, d[n][1] = d[n][3] = sum[n].y;
-                        }
-#pragma unroll
-                        for (int w = 0; w < WORDS; ++w) {
-                            // words of rows g and g + 8: a block holds two words of each
-                            const uint4 block = *(const uint4 *)(codes + r * 2048 + (j * WORDS + w) / 2 * 512);
-                            const uint2 q = (j * WORDS + w) % 2 ? make_uint2(block.z, block.w) : make_uint2(block.x, block.y);
-                            const uint32_t qx8 = q.x >> 8, qy8 = q.y >> 8;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16(d[n], q.x & 0x000f000fu, q.y & 0x000f000fu, q.x & 0x00f000f0u, q.y & 0x00f000f0u, x[w][n].x, x[w][n].y);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16(d[n], qx8 & 0x000f000fu, qy8 & 0x000f000fu, qx8 & 0x00f000f0u, qy8 & 0x00f000f0u, x[w][n].z, x[w][n].w);
+                            const uint32_t z = *(const uint16_t *)(zeros + r * ZPS + j * 2);
+                            z_lo *= byte_value<0>(z), z_hi *= byte_value<1>(z);
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            fma_pair(acc[r][n][0], acc[r][n][1], s_lo, d[n][0], d[n][1]);
-                            fma_pair(acc[r][n][2], acc[r][n][3], s_hi, d[n][2], d[n][3]);
+                            fma_pair(acc[r][n][0], acc[r][n][1], s_lo, d[r][n][0], d[r][n][1]);
+                            fma_pair(acc[r][n][2], acc[r][n][3], s_hi, d[r][n][2], d[r][n][3]);
+                            fma_pair(acc[r][n][0], acc[r][n][1], z_lo, sum[n].x, sum[n].y);
+                            fma_pair(acc[r][n][2], acc[r][n][3], z_hi, sum[n].x, sum[n].y);
                         }
                     }
                 }
@@ -318,29 +342,48 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     }
 }
 
+// Columns of x that fit beside the rings of W warps of S slots.
+template <int NT, int GROUP, bool ZEROS, int W, int S> constexpr int q4_room()
+{
+    constexpr long long left = 227 * 1024 - NT * 64 - (long long)W * S * kStage<GROUP, ZEROS>;
+    static_assert(left >= NT * 544 * kCols / 32, "a step of x fits");
+    static_assert(S * kStage<GROUP, ZEROS> >= NT * 512, "the parts' sums fit the rings");
+    return (int)(left / (NT * 544) * 32 / kCols * kCols);   // 512 + 32 bytes per 32 columns and 8 rows
+}
+
+template <int NT, int GROUP, bool ZEROS, int W, int S> cudaError_t launch_q4_warps(const Q4Params &p, Q4Plan plan, cudaStream_t s)
+{
+    // all of x in shared memory, or in chunks that every CTA goes through for each round
+    plan.chunk = std::min((p.K + kCols - 1) / kCols * kCols, q4_room<NT, GROUP, ZEROS, W, S>());
+    const size_t smem = (size_t)W * S * kStage<GROUP, ZEROS> + (size_t)plan.chunk / 32 * NT * 544;
+    cudaError_t e = allow_smem((const void *)k_q4_matvec<NT, GROUP, ZEROS, W, S>, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(std::min(sm_count(), plan.tiles), (p.B + NT * 8 - 1) / (NT * 8));
+    k_q4_matvec<NT, GROUP, ZEROS, W, S><<<grid, W * 32, smem, s>>>(p, plan);
+    return cudaGetLastError();
+}
+
+// 12 warps where each has more than a round of tiles, else 8, whose CTAs have less to set
+// up (262144 x 1536, 8 rows: 12 warps 43.3, 16 warps 45.5 us; 50021 x 2592, 23 rows: 43
+// with 12, 55 with 8, 53 with 16; 30000 x 2048, 8 rows: 14.6 with 12, 12.5 with 8, 16.7
+// with 16).  Three slots if x fits beside them (262144 x 1536, 8 rows: 45.3 with two).  With
+// x in chunks 8 warps are ahead up to 8 batch rows (65536 x 8192: 70 against 93 us), 12
+// above (90000 x 4096, 32 rows: 111 against 123).
 template <int NT, int GROUP, bool ZEROS> cudaError_t launch_q4(const Q4Params &p, cudaStream_t s)
 {
-    // 16 warps leave 128 registers a thread, which holds the sums of 16 batch rows
-    constexpr int W = NT <= 2 ? 16 : 12;
-    constexpr size_t most = 227 * 1024 - NT * 64, ring = W * kSlots * kStage;
-    static_assert(ring >= W * NT * 512, "the sums fit the rings");
     Q4Plan plan{};
     plan.tiles = p.M / 16 + (p.M % 16 != 0);
+    plan.parts = 1;
     const int sms = sm_count(), per_cta = (plan.tiles + sms - 1) / sms;
+    if (per_cta > 8 * kTiles) {
+        if (p.K <= q4_room<NT, GROUP, ZEROS, 12, 3>()) return launch_q4_warps<NT, GROUP, ZEROS, 12, 3>(p, plan, s);
+        if (NT > 1 || p.K <= q4_room<NT, GROUP, ZEROS, 12, 2>())
+            return launch_q4_warps<NT, GROUP, ZEROS, 12, 2>(p, plan, s);
+    }
     // few tiles per CTA: its warps share the rows' columns instead, as long as each then has
     // one tile at most
-    plan.parts = 1;
-    while (W % (plan.parts * 2) == 0 && per_cta * plan.parts * 2 <= W && plan.parts < 16) plan.parts *= 2;
-    // all of x in shared memory, or in chunks that every CTA goes through for each round
-    const size_t per_word = NT * (512 + 32);
-    plan.chunk = (p.K + kCols - 1) / kCols * kCols;
-    if (p.K / 32 * per_word > most - ring) plan.chunk = (int)((most - ring) / per_word) * 32 / kCols * kCols;
-    const size_t smem = ring + (size_t)std::min(plan.chunk, p.K) / 32 * per_word;
-    cudaError_t e = allow_smem((const void *)k_q4_matvec<NT, GROUP, ZEROS, W>, smem);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(std::min(sms, plan.tiles), (p.B + NT * 8 - 1) / (NT * 8));
-    k_q4_matvec<NT, GROUP, ZEROS, W><<<grid, W * 32, smem, s>>>(p, plan);
-    return cudaGetLastError();
+    while (per_cta * plan.parts * 2 <= 8) plan.parts *= 2;
+    return launch_q4_warps<NT, GROUP, ZEROS, 8, 3>(p, plan, s);
 }
 
 template <int NT, int GROUP> cudaError_t launch_q4_zeros(const Q4Params &p, cudaStream_t s)
