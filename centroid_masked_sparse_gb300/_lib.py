@@ -126,7 +126,7 @@ SIGNATURES = {
     "mtp_q4_pack": (_i32, [_QP, _p, _i64, _p, _p, _p, _sz, _p]),
     "mtp_q4_quantize": (_i32, [_p, _i64, _i32, _i32, _i32, _i32, _p, _i64, _p, _p, _p]),
     "mtp_kv_append": (_i32, [_KP, _SP, _p, _i64, _i64, _p, _i64, _i64, _p]),
-    "mtp_kv_attention_workspace_bytes": (_sz, [_KP, _SP, _i32, _i32]),
+    "mtp_kv_attention_workspace_bytes": (_sz, [_KP, _SP, _i32, _i32, _i32]),
     "mtp_kv_attention": (_i32, [_KP, _SP, _p, _i64, _i64, _i32, _i32, _i32, _f32, _p, _p, _p, _sz, _p]),
     "mtp_token_logprobs": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _f32, _i32, _p, _p, _p, _p, _p, _p, _i32, _p]),
     "mtp_token_logprobs_backward": (_i32, [_p, _i32, _i64, _i32, _i32, _p, _f32, _p, _p, _p, _p, _p, _i64, _i32, _p]),

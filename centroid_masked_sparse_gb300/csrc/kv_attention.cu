@@ -1,83 +1,558 @@
 // Attention of one or a few query tokens per sequence over the paged 8-bit cache.
+//
+// Mathematics.  For a query row (a query token and a head), s_j = scale * k_scale * (q . c_j)
+// over key codes c_j, p_j = 2^(s_j - m) in units of log2, o = sum p_j v_scale v_j / sum p_j.
+// Both products run on the tensor cores (mma m16n8k16, fp16 in, fp32 sums) with the codes as
+// the 16-row operand: S^T = K Q^T, 16 tokens by 8 query rows, and O^T = V^T P^T, 16 columns
+// of the head by 8 query rows, so the heads that share a kv head and a call's query tokens
+// fill the 8 columns.  Codes become fp16 as follows:
+//  - int8: the byte c + 128, masked in place, is the fp16 subnormal (c + 128) * 2^-24; the
+//    128 * sum q (128 * sum p) leaves the sum through its start, in fp32;
+//  - e4m3: cvt to fp16, exact.
+// q, which has 8 significant bits, is fp16 times a power of two per row; p is rounded to
+// fp16's 11 bits, and the same rounded p make the denominator.  The sums of a block of 16
+// tokens start at zero and are added, times v_scale, to the row's in fp32: blocks have their
+// own scales, and sums of 128 + c would otherwise outgrow what they are to hold.  m is the
+// row's maximum so far, or up to 8 below it: p stays below 2^8, and most blocks need no
+// maximum across lanes.
+//
+// Split.  A warp reads blocks of 16 tokens, eight kilobytes of codes ahead, each lane the
+// pieces of its own operands (cp.async into its own slots: no barrier).  The CTAs of an item
+// (a sequence, a kv head, a tile of query rows) share its blocks; eight of them form a
+// cluster and join their sums through distributed shared memory, each one slice of the
+// head's columns.  Only an item with more than one cluster goes through global memory: the
+// last cluster to arrive, per slice, adds the others' sums in their order.
+#include <algorithm>
+
 #include "lm_ops.h"
 
 namespace mtp {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
+constexpr int kW = 4;            // warps of a CTA
+constexpr int kStage = 8192;     // bytes of codes of a step
+constexpr int kMinBlocks = 16;   // blocks of 16 tokens that a CTA should have at least
+constexpr int kMaxCluster = 8;
 
-// One CTA per (query token, head); each warp takes every fourth cached token and keeps a
-// running maximum, sum and weighted value; the warps' results are joined at the end.
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads) k_kv_attention(KvAttentionParams p)
+template <bool INT8> __device__ __forceinline__ void key_operands(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    constexpr int E = D / 32, W = kAttnThreads / 32;
+    if (INT8) {   // bytes (0, 2) and (1, 3)
+        lo = (w & 0x00ff00ffu) ^ 0x00800080u;
+        hi = (w >> 8 & 0x00ff00ffu) ^ 0x00800080u;
+    } else {      // bytes (0, 1) and (2, 3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    }
+}
+
+// Bytes 0..3 of two tokens' words: pairs (a_i, b_i).
+template <bool INT8> __device__ __forceinline__ void value_operands(uint32_t a, uint32_t b, uint32_t (&v)[4])
+{
+    const uint32_t x = __byte_perm(a, b, INT8 ? 0x5410 : 0x5140), y = __byte_perm(a, b, INT8 ? 0x7632 : 0x7362);
+    key_operands<INT8>(x, v[0], v[1]);
+    key_operands<INT8>(y, v[2], v[3]);
+}
+
+// D: columns of a head; NT: query rows / 8.
+template <int D, bool INT8, int NT>
+__global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAttentionParams p)
+{
+    constexpr int U = kStage / (32 * D);       // blocks of 16 tokens in a step
+    constexpr int J = D / 64;                  // pieces of 64 columns of a key
+    constexpr int MT = D / 16;                 // tiles of 16 columns of a value
+    constexpr int E = D < 128 ? D / 8 : 16;    // columns of a lane in a piece of 128 (64)
+    constexpr int R = NT * 8;
+    constexpr float UNIT = INT8 ? 16777216.f : 1.f;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_factor[R], s_bias[R];
+    __shared__ float s_stat[3][kW][R];         // maximum, sum of rounded p, sum of p of each warp
+    __shared__ float s_total[3][R];            // the same of the CTA, read by the cluster
+    __shared__ float s_weight[kMaxCluster][R];
+    __shared__ uint32_t s_last;
     const KvParams &c = p.c;
-    __shared__ float s_m[W], s_l[W], s_o[W][D];
-    const int b = blockIdx.y, head = blockIdx.z, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int share = p.heads / c.kv_heads;
+
+    // the item and its rows; everything that ends the kernel early holds for the whole cluster
+    const int split = blockIdx.x % p.splits;
+    const long long item = blockIdx.x / p.splits;
+    const int h = (int)(item / p.row_tiles % c.kv_heads), b = (int)(item / p.row_tiles / c.kv_heads);
     int row0, n;
     kv_rows(c, b, &row0, &n);
-    if ((int)blockIdx.x >= n) return;
-    const long long row = row0 + blockIdx.x;
-    const int h = head / (p.heads / c.kv_heads);
-    const long long P = c.page_tokens;
-    long long length = __ldg(c.lengths + b);
-    const long long here = length - n + blockIdx.x;
-    if (length < 0 || length > c.table_width * P) {
-        if (c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
-    }
-    const long long first = p.window > 0 ? max(0ll, here - p.window + 1) : 0, end = min(here + 1, c.table_width * P);
+    const int r0 = (int)(item % p.row_tiles) * R, live = min(R, n * share - r0);
+    if (live <= 0) return;
+    const long long cap = (long long)c.table_width * c.page_tokens, length = __ldg(c.lengths + b);
+    if ((length < 0 || length > cap) && c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
+    // query i stands at position base + i; positions [lo, end) are seen by some row
+    const long long base = length - n;
+    const int q_lo = r0 / share, q_hi = (r0 + live - 1) / share;
+    const int lo = p.window > 0 ? (int)max(0ll, base + q_lo - p.window + 1) : 0;
+    const int end = (int)max(0ll, min(base + q_hi + 1, cap));
+    const int b_lo = lo / 16, blocks = end > lo ? (end + 15) / 16 - b_lo : 0;
+    const int csize = (int)cluster_size(), crank = (int)cluster_rank();
+    const int used = min(p.splits, max(1, (blocks + kMinBlocks - 1) / kMinBlocks));
+    const int clusters = (used + csize - 1) / csize, ck = split / csize;
+    if (ck >= clusters) return;
+    const int parts = clusters * csize;
+    const int s_lo = b_lo + (int)((long long)blocks * split / parts), s_hi = b_lo + (int)((long long)blocks * (split + 1) / parts);
 
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
+    // loads: a lane copies what it will read.  Keys: pieces (j, row half), 16 bytes of token
+    // g (+ 8); values: of tokens 2t, 2t + 1, 2t + 8, 2t + 9, the columns of g.
+    uint8_t *ring = smem + warp * 2 * kStage + lane * 16;
+    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+    const int page_blocks = c.page_tokens / 16;
+    const int32_t *table = c.table + b * c.ld_table;
+    int n_page[U];
+    float n_ks[U], n_vs[U];
+    bool n_ok[U];
+    auto fetch = [&](int it) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) q[e] = bf16_value(p.q[row * p.q_token + head * p.q_head + e * 32 + lane]);
-    for (long long t = first + warp; t < end; t += W) {
-        const int page = __ldg(c.table + b * c.ld_table + t / P);
-        if (page < 0 || page >= c.pages) {
-            if (c.err && lane == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
-            continue;
+        for (int u = 0; u < U; ++u) {
+            const int block = s_lo + (it * kW + warp) * U + u;
+            n_page[u] = block < s_hi ? __ldg(table + block / page_blocks) : -1;
         }
-        const long long ph = (long long)page * c.kv_heads + h, at = (ph * P + t % P) * D;
-        float s = 0.f;
+    };
+    auto load = [&](int it) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], kv_value(c.k_codes[at + e * 32 + lane], c.format), s);
-        s = warp_sum(s) * p.scale * c.k_scales[ph];
-        const float up = fmaxf(m, s), keep = up == -INFINITY ? 1.f : expf(m - up), w = up == -INFINITY ? 0.f : expf(s - up);
-        m = up;
-        l = l * keep + w;
+        for (int u = 0; u < U; ++u) {
+            const int block = s_lo + (it * kW + warp) * U + u, page = n_page[u];
+            n_ok[u] = page >= 0 && page < c.pages;
+            if (!n_ok[u]) {
+                if (block < s_hi && c.err && lane == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
+                continue;
+            }
+            const long long ph = (long long)page * c.kv_heads + h;
+            const long long at = (ph * c.page_tokens + block % page_blocks * 16) * D;
+            n_ks[u] = __ldg(c.k_scales + ph);
+            n_vs[u] = __ldg(c.v_scales + ph);
+            const int pos = block * 16;
+            const bool whole = pos >= lo && pos + 16 <= end;
+            // tokens outside [lo, end) are not read: zeros take their place
+            auto bytes = [&](int token) { return whole || (pos + token >= lo && pos + token < end) ? 16 : 0; };
+            uint32_t dst = ring_s + (it & 1) * kStage + u * 32 * D;
+            const uint8_t *k = c.k_codes + at + g * D + t * 16;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * c.v_scales[ph] * kv_value(c.v_codes[at + e * 32 + lane], c.format);
+            for (int half = 0; half < 2; ++half) {
+                const int size = bytes(g + half * 8);
+#pragma unroll
+                for (int j = 0; j < J; ++j) cp_async16_part(dst + (j * 2 + half) * 512, k + half * 8 * D + j * 64, size);
+            }
+            dst += 16 * D;
+            const uint8_t *v = c.v_codes + at + 2 * t * D + g * E;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int off = i % 2 + i / 2 * 8, size = bytes(2 * t + off);
+                if (D < 128) {
+                    cp_async8_part(dst + i / 2 * 512 + i % 2 * 8, v + off * D, size / 2);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < D / 128; ++j) cp_async16_part(dst + (j * 4 + i) * 512, v + off * D + j * 128, size);
+                }
+            }
+        }
+    };
+    fetch(0);
+    load(0);
+    cp_async_commit();
+    fetch(1);
+
+    // queries: a warp takes a row, finds its power of two and writes it in the operand's order
+    uint4 *s_q = (uint4 *)(smem + kW * 2 * kStage);   // [piece of 64][half of a lane's 16][NT][lane]
+    for (int r = warp; r < R; r += kW) {
+        const int row = r0 + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < live && lane < D / 8)
+            v = ld_ro16(p.q + (long long)(row0 + row / share) * p.q_token + (long long)(h * share + row % share) * p.q_head + lane * 8);
+        uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        top = __reduce_max_sync(~0u, max(top >> 16, top & 0xffffu));
+        const uint32_t e = fp16_factor_field(top);
+        const float f = __uint_as_float(e << 23);
+        const float x0 = bf_lo(v.x) * f, x1 = bf_hi(v.x) * f, x2 = bf_lo(v.y) * f, x3 = bf_hi(v.y) * f;
+        const float x4 = bf_lo(v.z) * f, x5 = bf_hi(v.z) * f, x6 = bf_lo(v.w) * f, x7 = bf_hi(v.w) * f;
+        const float sum = warp_sum(((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7)));
+        if (lane < D / 8)   // columns 8 * lane of the row: piece lane / 8, lane (r % 8, lane % 8 / 2)
+            s_q[((lane / 8 * 2 + lane % 2) * NT + r / 8) * 32 + r % 8 * 4 + lane % 8 / 2] =
+                INT8 ? make_uint4(half_pair(x0, x2), half_pair(x1, x3), half_pair(x4, x6), half_pair(x5, x7))
+                     : make_uint4(half_pair(x0, x1), half_pair(x2, x3), half_pair(x4, x5), half_pair(x6, x7));
+        if (lane == 0) {
+            s_factor[r] = p.scale * 1.44269504088896341f * fp16_factor_inverse(e);
+            s_bias[r] = sum * (-128.f / 16777216.f);
+        }
     }
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
     __syncthreads();
-    m = s_m[0];
-    for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w]);
-    l = 0.f;
-    for (int w = 0; w < W; ++w) l += m == -INFINITY ? s_l[w] : expf(s_m[w] - m) * s_l[w];
-    for (int d = threadIdx.x; d < D; d += kAttnThreads) {
-        float v = 0.f;
-        for (int w = 0; w < W; ++w) v += m == -INFINITY ? 0.f : expf(s_m[w] - m) * s_o[w][d];
-        p.out[(row * p.heads + head) * D + d] = bf16_bits(l == 0.f ? 0.f : v / l);
+    uint4 q[J * 2][NT];
+#pragma unroll
+    for (int i = 0; i < J * 2; ++i)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) q[i][m] = s_q[(i * NT + m) * 32 + lane];
+
+    // this lane's columns: query rows m * 8 + 2t + e
+    float factor[NT][2], bias[NT][2], top[NT][2], l_round[NT][2], l_sum[NT][2], o[NT][MT][4];
+    int here[NT][2];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = m * 8 + 2 * t + e;
+            factor[m][e] = s_factor[r] * UNIT;
+            bias[m][e] = INT8 ? s_bias[r] : 0.f;
+            here[m][e] = (int)min(base + (r0 + min(r, live - 1)) / share, cap);
+            top[m][e] = -INFINITY;
+            l_round[m][e] = l_sum[m][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.f;
     }
-    if (p.lse && threadIdx.x == 0) p.lse[row * p.heads + head] = l == 0.f ? -INFINITY : m + logf(l);
+    // blocks inside [clear_lo, clear_hi) are seen whole by every row
+    const long long clear_lo = p.window > 0 ? max(0ll, base + q_hi - p.window + 1) : 0, clear_hi = min(base + q_lo + 1, cap);
+
+    const int steps = (s_hi - s_lo + kW * U - 1) / (kW * U);
+    for (int it = 0; it < steps; ++it) {
+        cp_async_wait<0>();
+        float ks[U], vs[U];
+        bool ok[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) ks[u] = n_ks[u], vs[u] = n_vs[u], ok[u] = n_ok[u];
+        load(it + 1);
+        cp_async_commit();
+        fetch(it + 2);
+        const uint8_t *stage = ring + (it & 1) * kStage;
+
+        float s[U][NT][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!ok[u]) {
+#pragma unroll
+                for (int m = 0; m < NT; ++m) s[u][m][0] = s[u][m][1] = s[u][m][2] = s[u][m][3] = -INFINITY;
+                continue;
+            }
+            float d[NT][4];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint4 x = *(const uint4 *)(stage + u * 32 * D + j * 1024), y = *(const uint4 *)(stage + u * 32 * D + j * 1024 + 512);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a0, a1, a2, a3;
+                    key_operands<INT8>(xw[i], a0, a2);
+                    key_operands<INT8>(yw[i], a1, a3);
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) {
+                        const uint4 v = q[j * 2 + i / 2][m];
+                        const uint32_t b0 = i % 2 ? v.z : v.x, b1 = i % 2 ? v.w : v.y;
+                        if (j == 0 && i == 0)
+                            mma_f16_from(d[m], a0, a1, a2, a3, b0, b1, bias[m][0], bias[m][1]);
+                        else
+                            mma_f16(d[m], a0, a1, a2, a3, b0, b1);
+                    }
+                }
+            }
+            const int pos = (s_lo + (it * kW + warp) * U + u) * 16;
+#pragma unroll
+            for (int m = 0; m < NT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][m][e] = d[m][e] * (factor[m][e % 2] * ks[u]);
+            if (pos < clear_lo || pos + 16 > clear_hi) {
+#pragma unroll
+                for (int m = 0; m < NT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = pos + g + e / 2 * 8;
+                        if (at > here[m][e % 2] || at >= end || (p.window > 0 && here[m][e % 2] - at >= p.window)) s[u][m][e] = -INFINITY;
+                    }
+            }
+        }
+
+        // a new reference where a score is over 8 above the old one
+        bool up = false;
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float most = fmaxf(s[0][m][e], s[0][m][e + 2]);
+#pragma unroll
+                for (int u = 1; u < U; ++u) most = fmaxf(most, fmaxf(s[u][m][e], s[u][m][e + 2]));
+                up |= most > top[m][e] + 8.f;
+            }
+        if (__any_sync(~0u, up)) {
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float most = fmaxf(s[0][m][e], s[0][m][e + 2]);
+#pragma unroll
+                    for (int u = 1; u < U; ++u) most = fmaxf(most, fmaxf(s[u][m][e], s[u][m][e + 2]));
+                    most = fmaxf(most, __shfl_xor_sync(~0u, most, 4));
+                    most = fmaxf(most, __shfl_xor_sync(~0u, most, 8));
+                    most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
+                    most = fmaxf(most, top[m][e]);
+                    keep[e] = most == top[m][e] ? 1.f : exp2_fast(top[m][e] - most);
+                    top[m][e] = most;
+                    l_round[m][e] *= keep[e];
+                    l_sum[m][e] *= keep[e];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) o[m][i][0] *= keep[0], o[m][i][1] *= keep[1], o[m][i][2] *= keep[0], o[m][i][3] *= keep[1];
+            }
+        }
+
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!ok[u]) continue;
+            uint32_t b0[NT], b1[NT];
+            float start[NT][2];
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float from = top[m][e % 2] == -INFINITY ? 0.f : top[m][e % 2];   // no token of the row yet
+                    w[e] = exp2_fast(s[u][m][e] - from);
+                }
+                l_sum[m][0] += w[0] + w[2];
+                l_sum[m][1] += w[1] + w[3];
+                b0[m] = transpose_8x8(half_pair(w[0], w[1]));
+                b1[m] = transpose_8x8(half_pair(w[2], w[3]));
+                float l[4];
+                constexpr uint32_t ones = 0x3c003c00u;
+                mma_f16_first(l, ones, ones, ones, ones, b0[m], b1[m]);
+                l_round[m][0] += l[0];
+                l_round[m][1] += l[1];
+                start[m][0] = INT8 ? l[0] * (-128.f / 16777216.f) : 0.f;
+                start[m][1] = INT8 ? l[1] * (-128.f / 16777216.f) : 0.f;
+            }
+            const float scale = vs[u] * UNIT;
+            const uint8_t *values = stage + u * 32 * D + 16 * D;
+#pragma unroll
+            for (int j = 0; j < (D < 128 ? 1 : D / 128); ++j) {
+                uint32_t w[4][E / 4];   // words of the four tokens
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (D < 128) {
+                        const uint2 v = *(const uint2 *)(values + i / 2 * 512 + i % 2 * 8);
+                        w[i][0] = v.x, w[i][1] = v.y;
+                    } else {
+                        const uint4 v = *(const uint4 *)(values + (j * 4 + i) * 512);
+                        w[i][0] = v.x, w[i][1] = v.y, w[i][2 % (E / 4)] = v.z, w[i][3 % (E / 4)] = v.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    uint32_t lo4[4], hi4[4];
+                    value_operands<INT8>(w[0][i], w[1][i], lo4);
+                    value_operands<INT8>(w[2][i], w[3][i], hi4);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int m = 0; m < NT; ++m) {
+                            float d[4];
+                            mma_f16_from(d, lo4[half * 2], lo4[half * 2 + 1], hi4[half * 2], hi4[half * 2 + 1], b0[m], b1[m], start[m][0],
+                                         start[m][1]);
+                            float(&acc)[4] = o[m][j * 8 + i * 2 + half];
+                            fma_pair(acc[0], acc[1], scale, d[0], d[1]);
+                            fma_pair(acc[2], acc[3], scale, d[2], d[3]);
+                        }
+                }
+            }
+        }
+    }
+
+    // Join the warps.  The sums take the rings' place, columns c of lane group g at word
+    // (8c + g) ^ (8 (r / 2 % 4)) of their piece, which keeps a warp's stores off each other's banks.
+    cp_async_wait<0>();
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = l_sum[m][e];
+            l += __shfl_xor_sync(~0u, l, 4);
+            l += __shfl_xor_sync(~0u, l, 8);
+            l += __shfl_xor_sync(~0u, l, 16);
+            if (g == 0) {
+                const int r = m * 8 + 2 * t + e;
+                s_stat[0][warp][r] = top[m][e], s_stat[1][warp][r] = l_round[m][e], s_stat[2][warp][r] = l;
+            }
+        }
+    __syncthreads();
+    float *sums = (float *)smem;   // [warp][R][D]
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = i % 8 * 2 + e / 2, r = m * 8 + 2 * t + e % 2;
+                sums[(warp * R + r) * D + i / 8 * 128 + ((col * 8 + g) ^ (t * 8))] = o[m][i][e];
+            }
+    auto weight = [](float m, float most) { return m == -INFINITY ? 0.f : exp2_fast(m - most); };
+    __syncthreads();
+    if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        float most = -INFINITY, l = 0.f, e = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) most = fmaxf(most, s_stat[0][w][r]);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            const float f = weight(s_stat[0][w][r], most);
+            l += f * s_stat[1][w][r], e += f * s_stat[2][w][r];
+            s_stat[0][w][r] = f;
+        }
+        s_total[0][r] = most, s_total[1][r] = l, s_total[2][r] = e;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < live * D; i += kW * 32) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) v = fmaf(s_stat[0][w][i / D], sums[w * R * D + i], v);
+        sums[i] = v;
+    }
+    // Join the cluster: every CTA takes the columns [d_lo, d_lo + width).
+    if (csize > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        float most = -INFINITY, l = 0.f, e = 0.f;
+        for (int k = 0; k < csize; ++k) most = fmaxf(most, cluster_load(&s_total[0][r], k));
+        for (int k = 0; k < csize; ++k) {
+            const float f = weight(cluster_load(&s_total[0][r], k), most);
+            l = fmaf(f, cluster_load(&s_total[1][r], k), l), e = fmaf(f, cluster_load(&s_total[2][r], k), e);
+            s_weight[k][r] = f;
+        }
+        s_stat[0][0][r] = most, s_stat[1][0][r] = l, s_stat[2][0][r] = e;
+    }
+    __syncthreads();
+    const int width = D / csize, d_lo = crank * width;
+    auto place = [&](int r, int d) { return r * D + (d & ~127) + (((d & 127) % E * 8 + (d & 127) / E) ^ (r / 2 % 4 * 8)); };
+    auto finish = [&](int r, int d, float v, float l) {
+        const int row = r0 + r;
+        p.out[((long long)(row0 + row / share) * p.heads + h * share + row % share) * D + d] = bf16_bits(l == 0.f ? 0.f : v / l);
+    };
+    auto finish_lse = [&](int r, float most, float e) {
+        const int row = r0 + r;
+        if (p.lse)
+            p.lse[(long long)(row0 + row / share) * p.heads + h * share + row % share] =
+                e == 0.f ? -INFINITY : (most + log2f(e)) * 0.69314718055994531f;
+    };
+    float *partial = p.partial + (item * (p.splits / csize)) * (long long)(R * D + kMaxCluster * R * 3);
+    const long long stride = R * D + kMaxCluster * R * 3;   // of a cluster
+    for (int i = threadIdx.x; i < live * width; i += kW * 32) {
+        const int r = i / width, d = d_lo + i % width;
+        float v = 0.f;
+        for (int k = 0; k < csize; ++k) v = fmaf(s_weight[k][r], cluster_load(sums + place(r, d), k), v);
+        if (clusters == 1)
+            finish(r, d, v, s_stat[1][0][r]);
+        else
+            partial[ck * stride + r * D + d] = v;
+    }
+    if (threadIdx.x < live) {
+        const int r = threadIdx.x;
+        if (clusters > 1) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) partial[ck * stride + R * D + (crank * 3 + k) * R + r] = s_stat[k][0][r];
+        } else if (crank == 0) {
+            finish_lse(r, s_stat[0][0][r], s_stat[2][0][r]);
+        }
+    }
+    if (csize > 1) cluster_sync();   // the others may still be reading this CTA's sums
+    if (clusters == 1) return;
+
+    // Join the clusters: the last one to arrive, per slice of columns.
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t *ticket = p.tickets + item * kMaxCluster + crank;
+        s_last = atom_add_acq_rel(ticket, 1) == (uint32_t)clusters - 1;
+        if (s_last) *ticket = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
+    float *w_cluster = sums;   // [cluster][R]
+    if (threadIdx.x < live) {
+        const int r = threadIdx.x;
+        const float *stat = partial + R * D + crank * 3 * R + r;
+        float most = -INFINITY, l = 0.f, e = 0.f;
+        for (int k = 0; k < clusters; ++k) most = fmaxf(most, __ldcg(stat + k * stride));
+        for (int k = 0; k < clusters; ++k) {
+            const float f = weight(__ldcg(stat + k * stride), most);
+            l = fmaf(f, __ldcg(stat + k * stride + R), l), e = fmaf(f, __ldcg(stat + k * stride + 2 * R), e);
+            w_cluster[k * R + r] = f;
+        }
+        s_stat[1][0][r] = l;
+        if (crank == 0) finish_lse(r, most, e);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < live * width; i += kW * 32) {
+        const int r = i / width, d = d_lo + i % width;
+        float v = 0.f;
+        for (int k = 0; k < clusters; ++k) v = fmaf(w_cluster[k * R + r], __ldcg(partial + k * stride + r * D + d), v);
+        finish(r, d, v, s_stat[1][0][r]);
+    }
+}
+
+template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)
+{
+    const size_t smem = kW * 2 * kStage + D / 64 * 2 * NT * 512;
+    cudaError_t e = allow_smem((const void *)k_kv_attention<D, INT8, NT>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(plan.items * plan.splits));
+    cfg.blockDim = dim3(kW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = plan.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_kv_attention<D, INT8, NT>, p);
+}
+
+template <int D> cudaError_t launch_dim(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)
+{
+    if (p.c.format == MTP_KV_INT8) return plan.tiles8 == 1 ? launch<D, true, 1>(p, plan, s) : launch<D, true, 2>(p, plan, s);
+    return plan.tiles8 == 1 ? launch<D, false, 1>(p, plan, s) : launch<D, false, 2>(p, plan, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvAttentionParams &p, cudaStream_t s)
+KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int max_len)
 {
-    const int longest = p.c.starts ? p.c.max_tokens : p.c.tokens / p.c.batch;
-    const dim3 grid(longest, p.c.batch, p.heads);
-    if (p.c.dim == 64)
-        k_kv_attention<64><<<grid, kAttnThreads, 0, s>>>(p);
-    else if (p.c.dim == 128)
-        k_kv_attention<128><<<grid, kAttnThreads, 0, s>>>(p);
-    else
-        k_kv_attention<256><<<grid, kAttnThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    KvAttentionPlan plan{};
+    const long long longest_q = c.starts ? c.max_tokens : c.tokens / c.batch, rows = longest_q * (heads / c.kv_heads);
+    plan.tiles8 = rows <= 8 ? 1 : 2;
+    const int R = plan.tiles8 * 8;
+    plan.row_tiles = (int)((rows + R - 1) / R);
+    plan.items = (long long)c.batch * c.kv_heads * plan.row_tiles;
+    const long long cap = (long long)c.table_width * c.page_tokens;
+    long long seen = max_len > 0 ? std::min<long long>(max_len, cap) : cap;
+    if (window > 0) seen = std::min(seen, window + longest_q - 1);
+    // four rounds of CTAs where there are many items, whose lengths may differ
+    const long long slots = (long long)sm_count() * (plan.tiles8 == 1 ? 3 : 2);
+    const long long most = (seen / 16 + kMinBlocks) / kMinBlocks;
+    long long splits = plan.items >= slots / 2 ? 4 * slots / plan.items : slots / plan.items;
+    splits = std::max(1ll, std::min(splits, most));
+    plan.cluster = splits >= 5 ? 8 : splits >= 3 ? 4 : (int)splits;
+    splits = (splits + plan.cluster - 1) / plan.cluster * plan.cluster;
+    // without tickets for every item there is one cluster for each
+    if (plan.items * kMaxCluster > MTP_KV_WORKSPACE_ZEROED / 4) splits = plan.cluster;
+    plan.splits = (int)splits;
+    if (splits > plan.cluster)
+        plan.partial_floats = (size_t)plan.items * (splits / plan.cluster) * (R * c.dim + kMaxCluster * R * 3);
+    return plan;
+}
+
+cudaError_t launch_kv_attention(KvAttentionParams p, const KvAttentionPlan &plan, cudaStream_t s)
+{
+    if (plan.items * plan.splits > 0x7fffffff) return cudaErrorInvalidValue;
+    p.row_tiles = plan.row_tiles;
+    p.splits = plan.splits;
+    return p.c.dim == 64 ? launch_dim<64>(p, plan, s) : p.c.dim == 128 ? launch_dim<128>(p, plan, s) : launch_dim<256>(p, plan, s);
 }
 
 }  // namespace mtp

@@ -192,10 +192,13 @@ mtp_status mtp_kv_append(const mtp_kv_desc *d, const mtp_kv_batch *seqs, const v
     return cuda_status(launch_kv_append(p, (cudaStream_t)stream));
 }
 
-size_t mtp_kv_attention_workspace_bytes(const mtp_kv_desc *d, const mtp_kv_batch *seqs, int32_t heads, int32_t max_len)
+size_t mtp_kv_attention_workspace_bytes(const mtp_kv_desc *d, const mtp_kv_batch *seqs, int32_t heads, int32_t max_len,
+                                        int32_t window)
 {
-    if (check_cache(d, seqs) != MTP_OK || heads < 1 || heads % d->kv_heads != 0 || max_len < 0) return 0;
-    return MTP_KV_WORKSPACE_ZEROED;
+    if (check_cache(d, seqs) != MTP_OK || heads < 1 || heads % d->kv_heads != 0 || max_len < 0 || window < 0) return 0;
+    if (seqs->batch == 0 || seqs->tokens == 0) return MTP_KV_WORKSPACE_ZEROED;
+    DeviceScope dev(d->device);   // the split depends on the device's SMs
+    return MTP_KV_WORKSPACE_ZEROED + kv_attention_plan(kv_params(d, seqs), heads, window, max_len).partial_floats * sizeof(float);
 }
 
 mtp_status mtp_kv_attention(const mtp_kv_desc *d, const mtp_kv_batch *seqs, const void *q, int64_t q_token_stride,
@@ -209,13 +212,16 @@ mtp_status mtp_kv_attention(const mtp_kv_desc *d, const mtp_kv_batch *seqs, cons
     if (seqs->batch == 0 || seqs->tokens == 0) return MTP_OK;
     if ((st = check_strides(q, q_token_stride, q_head_stride)) != MTP_OK) return st;
     if (!out) return MTP_ERR_NULL;
-    if (!workspace || workspace_bytes < mtp_kv_attention_workspace_bytes(d, seqs, heads, max_len))
-        return MTP_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < MTP_KV_WORKSPACE_ZEROED) return MTP_ERR_WORKSPACE;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16)) return MTP_ERR_ALIGN;
     DeviceScope dev(d->device);
     if (!dev.ok) return MTP_ERR_CUDA;
     KvAttentionParams p{};
     p.c = kv_params(d, seqs);
+    const KvAttentionPlan plan = kv_attention_plan(p.c, heads, window, max_len);
+    if (workspace_bytes < MTP_KV_WORKSPACE_ZEROED + plan.partial_floats * sizeof(float)) return MTP_ERR_WORKSPACE;
+    p.tickets = (uint32_t *)workspace;
+    p.partial = (float *)((char *)workspace + MTP_KV_WORKSPACE_ZEROED);
     p.q = (const uint16_t *)q;
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;
@@ -224,7 +230,7 @@ mtp_status mtp_kv_attention(const mtp_kv_desc *d, const mtp_kv_batch *seqs, cons
     p.scale = scale;
     p.out = (uint16_t *)out;
     p.lse = lse;
-    return cuda_status(launch_kv_attention(p, (cudaStream_t)stream));
+    return cuda_status(launch_kv_attention(p, plan, (cudaStream_t)stream));
 }
 
 mtp_status mtp_token_logprobs(const void *logits, int32_t type, int64_t ld, int32_t rows, int32_t vocab,

@@ -70,8 +70,20 @@ struct KvAttentionParams {
     float scale;
     uint16_t *out;
     float *lse;              // or null
+    uint32_t *tickets;       // [items][8], zero between calls
+    float *partial;          // sums of the clusters of an item
+    int row_tiles, splits;   // set by the plan
 };
-cudaError_t launch_kv_attention(const KvAttentionParams &p, cudaStream_t s);
+// How a call is split: CTAs per item (a sequence, a kv head and a tile of query rows), in
+// clusters of `cluster`; the floats that the items' clusters exchange.
+struct KvAttentionPlan {
+    int tiles8;              // query rows of an item / 8 (1 or 2)
+    int row_tiles, splits, cluster;
+    long long items;
+    size_t partial_floats;
+};
+KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int max_len);
+cudaError_t launch_kv_attention(KvAttentionParams p, const KvAttentionPlan &plan, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Token log probabilities (logprobs.cu)
@@ -143,6 +155,114 @@ __device__ __forceinline__ uint8_t kv_code(float v, int format)
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
     return (uint8_t)r;
+}
+
+// 16 bytes from global to shared memory without a register or L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// d += a * b of m16n8k16, fp16 in, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// acc += s * d on a pair, with one instruction.
+__device__ __forceinline__ void fma_pair(float &acc0, float &acc1, float s, float d0, float d1)
+{
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%0, %1};\n"
+        " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+        : "+f"(acc0), "+f"(acc1)
+        : "f"(d0), "f"(d1), "f"(s));
+}
+
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The first `bytes` (0 or 16) of 16; the rest of the destination is zeroed.
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8_part(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// d = a * b + c with c[0] = c[2], c[1] = c[3] (the same for every row).
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1, float c0, float c1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, one row per quad of lanes.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The power of two that brings the bf16 value with these bits (no sign) to [2^14, 2^15),
+// as its exponent field, and its inverse.
+__device__ __forceinline__ uint32_t fp16_factor_field(uint32_t top) { return top == 0 ? 127u : min(254u, 268u - (top >> 7)); }
+__device__ __forceinline__ float fp16_factor_inverse(uint32_t e) { return __uint_as_float(e == 254u ? 0x00400000u : (254u - e) << 23); }
+
+// Thread-block clusters.
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of another CTA's shared memory: the address of one's own copy, and the rank.
+__device__ __forceinline__ float cluster_load(const float *own, uint32_t rank)
+{
+    const uint32_t addr = (uint32_t)__cvta_generic_to_shared(own);
+    float v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
 }
 
 }  // namespace mtp

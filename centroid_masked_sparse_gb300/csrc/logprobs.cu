@@ -15,13 +15,6 @@ template <typename T> __device__ __forceinline__ float logit_value(T v);
 template <> __device__ __forceinline__ float logit_value(float v) { return v; }
 template <> __device__ __forceinline__ float logit_value(uint16_t v) { return bf16_value(v); }
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // (larger logit, then lower id) as one unsigned key; 0 for a masked token.
 __device__ __forceinline__ unsigned long long top_key(float v, int id)
 {

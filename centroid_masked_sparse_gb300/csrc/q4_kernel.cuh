@@ -47,49 +47,10 @@ template <int GROUP> constexpr int kScales = 8 * (kCols / GROUP) * 4;
 template <int GROUP> constexpr int kZeros = kScales<GROUP> / 2;
 template <int GROUP, bool ZEROS> constexpr int kStage = kTiles * (2048 + kScales<GROUP> + (ZEROS ? kZeros<GROUP> : 0));
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same from zero.
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // Byte b of v (below 16) as a float: or-ed into 2^23, whose last place is 1.
 template <int B> __device__ __forceinline__ float byte_value(uint32_t v)
 {
     return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7650 + B)) - 8388608.f;
-}
-
-// acc += s * d on a pair, with one instruction.
-__device__ __forceinline__ void fma_pair(float &acc0, float &acc1, float s, float d0, float d1)
-{
-    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%0, %1};\n"
-        " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
-        : "+f"(acc0), "+f"(acc1)
-        : "f"(d0), "f"(d1), "f"(s));
-}
-
-__device__ __forceinline__ uint32_t half_pair(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // NT: batch rows / 8; GROUP: columns of a group; ZEROS: zero points; W: warps; S: slots of a
@@ -173,10 +134,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         top = max(top >> 16, top & 0xffffu);
         top = __reduce_max_sync(~0u, top);
         if (lane == 0) {
-            const uint32_t e = top == 0 ? 127u : min(254u, 268u - (top >> 7));   // exponent field of the factor
+            const uint32_t e = fp16_factor_field(top);
             s_factor[n] = __uint_as_float(e << 23);
             // a row that holds a NaN or an infinity gives NaN
-            s_inverse[n] = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float(e == 254u ? 0x00400000u : (254u - e) << 23);
+            s_inverse[n] = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fp16_factor_inverse(e);
         }
     }
     __syncwarp();

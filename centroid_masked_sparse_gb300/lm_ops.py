@@ -201,9 +201,9 @@ def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, s
                               v.data_ptr(), v.stride(0), v.stride(1), _stream(stream, cache.device)), "mtp_kv_append")
 
 
-def mtp_kv_attention_workspace_bytes(cache, page_table, lengths, tokens, heads, starts=None, max_q=None, max_len=0) -> int:
+def mtp_kv_attention_workspace_bytes(cache, page_table, lengths, tokens, heads, starts=None, max_q=None, max_len=0, window=0) -> int:
     seqs = _batch_desc(cache, page_table, lengths, starts, int(tokens), max_q)
-    return int(lib().mtp_kv_attention_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(seqs), int(heads), int(max_len)))
+    return int(lib().mtp_kv_attention_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(seqs), int(heads), int(max_len), int(window)))
 
 
 def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max_len=0, window=0, scale=None, out=None,
@@ -222,7 +222,7 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
     seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_q)
     desc, library = ctypes.byref(cache.desc), lib()
     if workspace is None:
-        workspace = cache.workspace(library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len),
+        workspace = cache.workspace(library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len, window),
                                     stream)
     check(library.mtp_kv_attention(desc, ctypes.byref(seqs), q.data_ptr(), q.stride(0), q.stride(1), heads, max_len,
                                    window, cache.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),

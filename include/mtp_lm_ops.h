@@ -199,7 +199,7 @@ MTP_API mtp_status mtp_kv_append(const mtp_kv_desc *desc, const mtp_kv_batch *se
  * Non-finite q, scales or e4m3 codes give what IEEE arithmetic gives. */
 #define MTP_KV_WORKSPACE_ZEROED 262144u
 MTP_API size_t mtp_kv_attention_workspace_bytes(const mtp_kv_desc *desc, const mtp_kv_batch *seqs, int32_t heads,
-                                                int32_t max_len);
+                                                int32_t max_len, int32_t window);
 MTP_API mtp_status mtp_kv_attention(const mtp_kv_desc *desc, const mtp_kv_batch *seqs, const void *q,
                                     int64_t q_token_stride, int64_t q_head_stride, int32_t heads, int32_t max_len,
                                     int32_t window, float scale, void *out, float *lse, void *workspace,

@@ -124,11 +124,11 @@ def test_kv_attention_refuses_no_descriptor(L):
 
 def test_kv_attention_workspace(L):
     from centroid_masked_sparse_gb300 import MTP_KV_WORKSPACE_ZEROED
-    need = L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 8, 0)
+    need = L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 8, 0, 0)
     assert need >= MTP_KV_WORKSPACE_ZEROED
-    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 5, 0) == 0
-    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv(head_dim=80)), ctypes.byref(seqs()), 8, 0) == 0
-    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 8, -1) == 0
+    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 5, 0, 0) == 0
+    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv(head_dim=80)), ctypes.byref(seqs()), 8, 0, 0) == 0
+    assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 8, -1, 0) == 0
 
 
 @pytest.mark.parametrize("kw,expect", [
