@@ -34,6 +34,7 @@ constexpr int kW = 4;            // warps of a CTA
 constexpr int kStage = 8192;     // bytes of codes of a step
 constexpr int kMinBlocks = 16;   // blocks of 16 tokens that a CTA should have at least
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSplits = 512;  // the clusters' statistics fit the place of a head of 64
 
 template <bool INT8> __device__ __forceinline__ void key_operands(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
@@ -66,36 +67,47 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
     constexpr float UNIT = INT8 ? 16777216.f : 1.f;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_factor[R], s_bias[R];
-    __shared__ float s_stat[3][kW][R];         // maximum, sum of rounded p, sum of p of each warp
+    __shared__ float s_stat[kW][3][R];         // maximum, sum of rounded p, sum of p of each warp
     __shared__ float s_total[3][R];            // the same of the CTA, read by the cluster
-    __shared__ float s_weight[kMaxCluster][R];
+    __shared__ float s_weight[kMaxCluster][R], s_joined[3][R];
     __shared__ uint32_t s_last;
     const KvParams &c = p.c;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int share = p.heads / c.kv_heads;
 
     // the item and its rows; everything that ends the kernel early holds for the whole cluster
-    const int split = blockIdx.x % p.splits;
-    const long long item = blockIdx.x / p.splits;
-    const int h = (int)(item / p.row_tiles % c.kv_heads), b = (int)(item / p.row_tiles / c.kv_heads);
+    const int split = blockIdx.x, b = blockIdx.z, h = blockIdx.y / p.row_tiles;
+    const long long item = (long long)b * gridDim.y + blockIdx.y;
+    const long long length = __ldg(c.lengths + b);
     int row0, n;
     kv_rows(c, b, &row0, &n);
-    const int r0 = (int)(item % p.row_tiles) * R, live = min(R, n * share - r0);
+    const int r0 = (blockIdx.y - h * p.row_tiles) * R, live = min(R, n * share - r0);
     if (live <= 0) return;
-    const long long cap = (long long)c.table_width * c.page_tokens, length = __ldg(c.lengths + b);
+    const int cap = c.table_width * c.page_tokens;
     if ((length < 0 || length > cap) && c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
     // query i stands at position base + i; positions [lo, end) are seen by some row
     const long long base = length - n;
     const int q_lo = r0 / share, q_hi = (r0 + live - 1) / share;
     const int lo = p.window > 0 ? (int)max(0ll, base + q_lo - p.window + 1) : 0;
-    const int end = (int)max(0ll, min(base + q_hi + 1, cap));
+    const int end = (int)max(0ll, min(base + q_hi + 1, (long long)cap));
     const int b_lo = lo / 16, blocks = end > lo ? (end + 15) / 16 - b_lo : 0;
     const int csize = (int)cluster_size(), crank = (int)cluster_rank();
     const int used = min(p.splits, max(1, (blocks + kMinBlocks - 1) / kMinBlocks));
     const int clusters = (used + csize - 1) / csize, ck = split / csize;
     if (ck >= clusters) return;
-    const int parts = clusters * csize;
-    const int s_lo = b_lo + (int)((long long)blocks * split / parts), s_hi = b_lo + (int)((long long)blocks * (split + 1) / parts);
+    const int parts = clusters * csize, per = blocks / parts, rest = blocks - per * parts;
+    const int s_lo = b_lo + per * split + min(split, rest), s_hi = s_lo + per + (split < rest);
+
+    // this warp's rows of queries, on their way while the first pages are looked up
+    constexpr int QR = R / kW;
+    uint4 q_in[QR];
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+        const int row = r0 + warp + i * kW;
+        q_in[i] = make_uint4(0, 0, 0, 0);
+        if (warp + i * kW < live && lane < D / 8)
+            q_in[i] = ld_ro16(p.q + (long long)(row0 + row / share) * p.q_token + (long long)(h * share + row % share) * p.q_head + lane * 8);
+    }
 
     // loads: a lane copies what it will read.  Keys: pieces (j, row half), 16 bytes of token
     // g (+ 8); values: of tokens 2t, 2t + 1, 2t + 8, 2t + 9, the columns of g.
@@ -103,27 +115,33 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
     const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
     const int page_blocks = c.page_tokens / 16;
     const int32_t *table = c.table + b * c.ld_table;
-    int n_page[U];
-    float n_ks[U], n_vs[U];
-    bool n_ok[U];
-    auto fetch = [&](int it) {
+    // of the step at hand, the next one, and the page and the block in it of the one after
+    float ks[U], vs[U], n_ks[U], n_vs[U];
+    bool ok[U], n_ok[U];
+    struct Place {
+        int page, block;
+    };
+    Place n_place[U];
+    auto fetch = [&](int it, Place (&to)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int block = s_lo + (it * kW + warp) * U + u;
-            n_page[u] = block < s_hi ? __ldg(table + block / page_blocks) : -1;
+            const int column = p.page_magic ? (int)__umulhi(block, p.page_magic) : block;   // block / page_blocks
+            to[u].page = block < s_hi ? __ldg(table + column) : -1;
+            to[u].block = block - column * page_blocks;
         }
     };
-    auto load = [&](int it) {
+    auto load = [&](int it, const Place (&from)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int block = s_lo + (it * kW + warp) * U + u, page = n_page[u];
+            const int block = s_lo + (it * kW + warp) * U + u, page = from[u].page;
             n_ok[u] = page >= 0 && page < c.pages;
             if (!n_ok[u]) {
                 if (block < s_hi && c.err && lane == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
                 continue;
             }
             const long long ph = (long long)page * c.kv_heads + h;
-            const long long at = (ph * c.page_tokens + block % page_blocks * 16) * D;
+            const long long at = (ph * c.page_tokens + from[u].block * 16) * D;
             n_ks[u] = __ldg(c.k_scales + ph);
             n_vs[u] = __ldg(c.v_scales + ph);
             const int pos = block * 16;
@@ -152,38 +170,50 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
             }
         }
     };
-    fetch(0);
-    load(0);
-    cp_async_commit();
-    fetch(1);
+    auto advance = [&] {
+#pragma unroll
+        for (int u = 0; u < U; ++u) ks[u] = n_ks[u], vs[u] = n_vs[u], ok[u] = n_ok[u];
+    };
+    {
+        Place first[U], second[U];
+        fetch(0, first);
+        fetch(1, second);
+        fetch(2, n_place);
+        load(0, first);
+        cp_async_commit();
+        advance();
+        load(1, second);
+        cp_async_commit();
+    }
 
-    // queries: a warp takes a row, finds its power of two and writes it in the operand's order
+    // each row's power of two, and the row in the operand's order
     uint4 *s_q = (uint4 *)(smem + kW * 2 * kStage);   // [piece of 64][half of a lane's 16][NT][lane]
-    for (int r = warp; r < R; r += kW) {
-        const int row = r0 + r;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < live && lane < D / 8)
-            v = ld_ro16(p.q + (long long)(row0 + row / share) * p.q_token + (long long)(h * share + row % share) * p.q_head + lane * 8);
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+        const int r = warp + i * kW;
+        const uint4 v = q_in[i];
         uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
         top = __reduce_max_sync(~0u, max(top >> 16, top & 0xffffu));
         const uint32_t e = fp16_factor_field(top);
         const float f = __uint_as_float(e << 23);
         const float x0 = bf_lo(v.x) * f, x1 = bf_hi(v.x) * f, x2 = bf_lo(v.y) * f, x3 = bf_hi(v.y) * f;
         const float x4 = bf_lo(v.z) * f, x5 = bf_hi(v.z) * f, x6 = bf_lo(v.w) * f, x7 = bf_hi(v.w) * f;
-        const float sum = warp_sum(((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7)));
         if (lane < D / 8)   // columns 8 * lane of the row: piece lane / 8, lane (r % 8, lane % 8 / 2)
             s_q[((lane / 8 * 2 + lane % 2) * NT + r / 8) * 32 + r % 8 * 4 + lane % 8 / 2] =
                 INT8 ? make_uint4(half_pair(x0, x2), half_pair(x1, x3), half_pair(x4, x6), half_pair(x5, x7))
                      : make_uint4(half_pair(x0, x1), half_pair(x2, x3), half_pair(x4, x5), half_pair(x6, x7));
+        const float sum = INT8 ? warp_sum(((x0 + x1) + (x2 + x3)) + ((x4 + x5) + (x6 + x7))) : 0.f;
         if (lane == 0) {
             s_factor[r] = p.scale * 1.44269504088896341f * fp16_factor_inverse(e);
             s_bias[r] = sum * (-128.f / 16777216.f);
         }
     }
     __syncthreads();
-    uint4 q[J * 2][NT];
+    // in registers, or read again for each block where the sums need these (D = 256, 16 rows)
+    constexpr bool QREG = D * NT <= 256;
+    uint4 q[QREG ? J * 2 : 1][NT];
 #pragma unroll
-    for (int i = 0; i < J * 2; ++i)
+    for (int i = 0; i < (QREG ? J * 2 : 1); ++i)
 #pragma unroll
         for (int m = 0; m < NT; ++m) q[i][m] = s_q[(i * NT + m) * 32 + lane];
 
@@ -197,7 +227,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
             const int r = m * 8 + 2 * t + e;
             factor[m][e] = s_factor[r] * UNIT;
             bias[m][e] = INT8 ? s_bias[r] : 0.f;
-            here[m][e] = (int)min(base + (r0 + min(r, live - 1)) / share, cap);
+            here[m][e] = (int)min(base + (r0 + min(r, live - 1)) / share, (long long)cap);
             top[m][e] = -INFINITY;
             l_round[m][e] = l_sum[m][e] = 0.f;
         }
@@ -205,18 +235,11 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
         for (int i = 0; i < MT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.f;
     }
     // blocks inside [clear_lo, clear_hi) are seen whole by every row
-    const long long clear_lo = p.window > 0 ? max(0ll, base + q_hi - p.window + 1) : 0, clear_hi = min(base + q_lo + 1, cap);
+    const long long clear_lo = p.window > 0 ? max(0ll, base + q_hi - p.window + 1) : 0, clear_hi = min(base + q_lo + 1, (long long)cap);
 
     const int steps = (s_hi - s_lo + kW * U - 1) / (kW * U);
     for (int it = 0; it < steps; ++it) {
-        cp_async_wait<0>();
-        float ks[U], vs[U];
-        bool ok[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) ks[u] = n_ks[u], vs[u] = n_vs[u], ok[u] = n_ok[u];
-        load(it + 1);
-        cp_async_commit();
-        fetch(it + 2);
+        cp_async_wait<1>();
         const uint8_t *stage = ring + (it & 1) * kStage;
 
         float s[U][NT][4];
@@ -227,7 +250,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
                 for (int m = 0; m < NT; ++m) s[u][m][0] = s[u][m][1] = s[u][m][2] = s[u][m][3] = -INFINITY;
                 continue;
             }
-            float d[NT][4];
+            float d[NT][4], d2[NT][4];   // two chains of products
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const uint4 x = *(const uint4 *)(stage + u * 32 * D + j * 1024), y = *(const uint4 *)(stage + u * 32 * D + j * 1024 + 512);
@@ -239,12 +262,14 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
                     key_operands<INT8>(yw[i], a1, a3);
 #pragma unroll
                     for (int m = 0; m < NT; ++m) {
-                        const uint4 v = q[j * 2 + i / 2][m];
+                        const uint4 v = QREG ? q[(j * 2 + i / 2) % (QREG ? J * 2 : 1)][m] : s_q[((j * 2 + i / 2) * NT + m) * 32 + lane];
                         const uint32_t b0 = i % 2 ? v.z : v.x, b1 = i % 2 ? v.w : v.y;
                         if (j == 0 && i == 0)
                             mma_f16_from(d[m], a0, a1, a2, a3, b0, b1, bias[m][0], bias[m][1]);
+                        else if (j == 0 && i == 1)
+                            mma_f16_first(d2[m], a0, a1, a2, a3, b0, b1);
                         else
-                            mma_f16(d[m], a0, a1, a2, a3, b0, b1);
+                            mma_f16(i % 2 ? d2[m] : d[m], a0, a1, a2, a3, b0, b1);
                     }
                 }
             }
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
 #pragma unroll
             for (int m = 0; m < NT; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[u][m][e] = d[m][e] * (factor[m][e % 2] * ks[u]);
+                for (int e = 0; e < 4; ++e) s[u][m][e] = (d[m][e] + d2[m][e]) * (factor[m][e % 2] * ks[u]);
             if (pos < clear_lo || pos + 16 > clear_hi) {
 #pragma unroll
                 for (int m = 0; m < NT; ++m)
@@ -357,10 +382,15 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
                 }
             }
         }
+        advance();
+        load(it + 2, n_place);   // into the slot just read, by the lane that read it
+        cp_async_commit();
+        fetch(it + 3, n_place);
     }
 
-    // Join the warps.  The sums take the rings' place, columns c of lane group g at word
-    // (8c + g) ^ (8 (r / 2 % 4)) of their piece, which keeps a warp's stores off each other's banks.
+    // Join the warps.  Their sums, relative to the CTA's maximum, take the rings' place, columns
+    // c of lane group g at word (8c + g) ^ (8 (r / 2 % 4)) of their piece of 128, which keeps a
+    // warp's stores off each other's banks.
     cp_async_wait<0>();
 #pragma unroll
     for (int m = 0; m < NT; ++m)
@@ -372,64 +402,66 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
             l += __shfl_xor_sync(~0u, l, 16);
             if (g == 0) {
                 const int r = m * 8 + 2 * t + e;
-                s_stat[0][warp][r] = top[m][e], s_stat[1][warp][r] = l_round[m][e], s_stat[2][warp][r] = l;
+                s_stat[warp][0][r] = top[m][e], s_stat[warp][1][r] = l_round[m][e], s_stat[warp][2][r] = l;
             }
         }
     __syncthreads();
+    auto weight = [](float m, float most) { return m == -INFINITY ? 0.f : exp2_fast(m - most); };
     float *sums = (float *)smem;   // [warp][R][D]
 #pragma unroll
-    for (int m = 0; m < NT; ++m)
+    for (int m = 0; m < NT; ++m) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = m * 8 + 2 * t + e;
+            float most = s_stat[0][0][r];
+#pragma unroll
+            for (int w = 1; w < kW; ++w) most = fmaxf(most, s_stat[w][0][r]);
+            f[e] = weight(top[m][e], most);
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int col = i % 8 * 2 + e / 2, r = m * 8 + 2 * t + e % 2;
-                sums[(warp * R + r) * D + i / 8 * 128 + ((col * 8 + g) ^ (t * 8))] = o[m][i][e];
+                sums[(warp * R + r) * D + i / 8 * 128 + ((col * 8 + g) ^ (t * 8))] = o[m][i][e] * f[e % 2];
             }
-    auto weight = [](float m, float most) { return m == -INFINITY ? 0.f : exp2_fast(m - most); };
-    __syncthreads();
-    if (threadIdx.x < R) {
-        const int r = threadIdx.x;
-        float most = -INFINITY, l = 0.f, e = 0.f;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) most = fmaxf(most, s_stat[0][w][r]);
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const float f = weight(s_stat[0][w][r], most);
-            l += f * s_stat[1][w][r], e += f * s_stat[2][w][r];
-            s_stat[0][w][r] = f;
+    }
+    // Row r's statistics of several parties, joined; the weights of theirs.
+    auto join = [&](int r, int count, const float (*stat)[3][R], float *weights, float *joined) {
+        float most = stat[0][0][r], l = 0.f, e = 0.f;
+#pragma unroll 8
+        for (int k = 1; k < count; ++k) most = fmaxf(most, stat[k][0][r]);
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+            const float f = weight(stat[k][0][r], most);
+            l = fmaf(f, stat[k][1][r], l), e = fmaf(f, stat[k][2][r], e);
+            if (weights) weights[k * R + r] = f;
         }
-        s_total[0][r] = most, s_total[1][r] = l, s_total[2][r] = e;
-    }
+        joined[0] = most, joined[R] = l, joined[2 * R] = e;
+    };
+    if (threadIdx.x < R) join(threadIdx.x, kW, s_stat, nullptr, s_total[0] + threadIdx.x);
     __syncthreads();
-    for (int i = threadIdx.x; i < live * D; i += kW * 32) {
-        float v = 0.f;
+    float4 *sums4 = (float4 *)sums;
+    for (int i = threadIdx.x; i < live * D / 4; i += kW * 32) {
+        float4 v = sums4[i];
 #pragma unroll
-        for (int w = 0; w < kW; ++w) v = fmaf(s_stat[0][w][i / D], sums[w * R * D + i], v);
-        sums[i] = v;
-    }
-    // Join the cluster: every CTA takes the columns [d_lo, d_lo + width).
-    if (csize > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    if (threadIdx.x < R) {
-        const int r = threadIdx.x;
-        float most = -INFINITY, l = 0.f, e = 0.f;
-        for (int k = 0; k < csize; ++k) most = fmaxf(most, cluster_load(&s_total[0][r], k));
-        for (int k = 0; k < csize; ++k) {
-            const float f = weight(cluster_load(&s_total[0][r], k), most);
-            l = fmaf(f, cluster_load(&s_total[1][r], k), l), e = fmaf(f, cluster_load(&s_total[2][r], k), e);
-            s_weight[k][r] = f;
+        for (int w = 1; w < kW; ++w) {
+            const float4 x = sums4[w * R * D / 4 + i];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
-        s_stat[0][0][r] = most, s_stat[1][0][r] = l, s_stat[2][0][r] = e;
+        sums4[i] = v;
     }
-    __syncthreads();
-    const int width = D / csize, d_lo = crank * width;
-    auto place = [&](int r, int d) { return r * D + (d & ~127) + (((d & 127) % E * 8 + (d & 127) / E) ^ (r / 2 % 4 * 8)); };
-    auto finish = [&](int r, int d, float v, float l) {
-        const int row = r0 + r;
-        p.out[((long long)(row0 + row / share) * p.heads + h * share + row % share) * D + d] = bf16_bits(l == 0.f ? 0.f : v / l);
+    // a word's column, and what becomes of a row's sum and statistics
+    auto column = [&](int r, int word) {
+        const int x = word % 128 ^ (r / 2 % 4 * 8);
+        return word / 128 * 128 + x % 8 * E + x / 8;
+    };
+    auto finish = [&](int r, int word, float4 v, float l) {
+        const int row = r0 + r, d = column(r, word);   // the next three words are the next three lane groups
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        uint16_t *out = p.out + ((long long)(row0 + row / share) * p.heads + h * share + row % share) * D + d;
+        out[0] = bf16_bits(v.x * f), out[E] = bf16_bits(v.y * f), out[2 * E] = bf16_bits(v.z * f), out[3 * E] = bf16_bits(v.w * f);
     };
     auto finish_lse = [&](int r, float most, float e) {
         const int row = r0 + r;
@@ -437,30 +469,59 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
             p.lse[(long long)(row0 + row / share) * p.heads + h * share + row % share] =
                 e == 0.f ? -INFINITY : (most + log2f(e)) * 0.69314718055994531f;
     };
-    float *partial = p.partial + (item * (p.splits / csize)) * (long long)(R * D + kMaxCluster * R * 3);
-    const long long stride = R * D + kMaxCluster * R * 3;   // of a cluster
-    for (int i = threadIdx.x; i < live * width; i += kW * 32) {
-        const int r = i / width, d = d_lo + i % width;
-        float v = 0.f;
-        for (int k = 0; k < csize; ++k) v = fmaf(s_weight[k][r], cluster_load(sums + place(r, d), k), v);
-        if (clusters == 1)
-            finish(r, d, v, s_stat[1][0][r]);
-        else
-            partial[ck * stride + r * D + d] = v;
+    if (csize == 1 && clusters == 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < live * D / 4; i += kW * 32) finish(i * 4 / D, i * 4 % D, sums4[i], s_total[1][i * 4 / D]);
+        if (threadIdx.x < live) finish_lse(threadIdx.x, s_total[0][threadIdx.x], s_total[2][threadIdx.x]);
+        return;
     }
-    if (threadIdx.x < live) {
-        const int r = threadIdx.x;
-        if (clusters > 1) {
+
+    // Join the cluster: every CTA takes a slice of a row's words, [crank * width, + width).
+    float (*stat)[3][R] = (float (*)[3][R])(sums + R * D);   // of the parties, in the other warps' place
+    cluster_sync();
+    {
+        float x[kMaxCluster * 3 * R / (kW * 32) + 1];
 #pragma unroll
-            for (int k = 0; k < 3; ++k) partial[ck * stride + R * D + (crank * 3 + k) * R + r] = s_stat[k][0][r];
-        } else if (crank == 0) {
-            finish_lse(r, s_stat[0][0][r], s_stat[2][0][r]);
+        for (int k = 0; k < kMaxCluster * 3 * R / (kW * 32) + 1; ++k) {
+            const int i = threadIdx.x + k * kW * 32;
+            x[k] = i < csize * 3 * R ? cluster_load(&s_total[0][0] + i % (3 * R), i / (3 * R)) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster * 3 * R / (kW * 32) + 1; ++k) {
+            const int i = threadIdx.x + k * kW * 32;
+            if (i < csize * 3 * R) (&stat[0][0][0])[i] = x[k];
         }
     }
-    if (csize > 1) cluster_sync();   // the others may still be reading this CTA's sums
-    if (clusters == 1) return;
+    __syncthreads();
+    if (threadIdx.x < R) join(threadIdx.x, csize, stat, s_weight[0], s_joined[0] + threadIdx.x);
+    __syncthreads();
+    const int width = D / csize;
+    const long long stride = R * D + kMaxCluster * R * 3;   // of a cluster's sums in global memory
+    float *partial = p.partial + item * (p.splits / csize) * stride;
+    for (int i = threadIdx.x; i < live * width / 4; i += kW * 32) {
+        const int r = i * 4 / width, word = crank * width + i * 4 % width;
+        float4 x[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) x[k] = cluster_load4(sums + r * D + word, k < csize ? k : 0);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+            const float f = k < csize ? s_weight[k][r] : 0.f;
+            if (k < csize) v.x = fmaf(f, x[k].x, v.x), v.y = fmaf(f, x[k].y, v.y), v.z = fmaf(f, x[k].z, v.z), v.w = fmaf(f, x[k].w, v.w);
+        }
+        if (clusters == 1)
+            finish(r, word, v, s_joined[1][r]);
+        else
+            *(float4 *)(partial + ck * stride + r * D + word) = v;
+    }
+    if (clusters == 1) {
+        if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
+        cluster_sync();   // the others may still be reading this CTA's sums
+        return;
+    }
+    for (int i = threadIdx.x; i < 3 * R; i += kW * 32) partial[ck * stride + R * D + crank * 3 * R + i] = s_joined[0][i];
+    cluster_sync();
 
-    // Join the clusters: the last one to arrive, per slice of columns.
+    // Join the clusters: the last one to arrive, per slice of columns, in the clusters' order.
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -471,27 +532,33 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
     }
     __syncthreads();
     if (!s_last) return;
-    float *w_cluster = sums;   // [cluster][R]
-    if (threadIdx.x < live) {
-        const int r = threadIdx.x;
-        const float *stat = partial + R * D + crank * 3 * R + r;
-        float most = -INFINITY, l = 0.f, e = 0.f;
-        for (int k = 0; k < clusters; ++k) most = fmaxf(most, __ldcg(stat + k * stride));
-        for (int k = 0; k < clusters; ++k) {
-            const float f = weight(__ldcg(stat + k * stride), most);
-            l = fmaf(f, __ldcg(stat + k * stride + R), l), e = fmaf(f, __ldcg(stat + k * stride + 2 * R), e);
-            w_cluster[k * R + r] = f;
-        }
-        s_stat[1][0][r] = l;
-        if (crank == 0) finish_lse(r, most, e);
-    }
+    for (int i = threadIdx.x; i < clusters * 3 * R; i += kW * 32)
+        (&stat[0][0][0])[i] = __ldcg(partial + i / (3 * R) * stride + R * D + crank * 3 * R + i % (3 * R));
+    float *weights = sums;   // [cluster][R]
     __syncthreads();
-    for (int i = threadIdx.x; i < live * width; i += kW * 32) {
-        const int r = i / width, d = d_lo + i % width;
-        float v = 0.f;
-        for (int k = 0; k < clusters; ++k) v = fmaf(w_cluster[k * R + r], __ldcg(partial + k * stride + r * D + d), v);
-        finish(r, d, v, s_stat[1][0][r]);
+    if (threadIdx.x < R) join(threadIdx.x, clusters, stat, weights, s_joined[0] + threadIdx.x);
+    __syncthreads();
+    // four words and every fourth cluster at a time, as the threads go
+    constexpr int LANES = 4;
+    for (int q0 = 0; q0 < live * width / 4; q0 += kW * 32 / LANES) {
+        const int i = q0 + threadIdx.x / LANES, from = threadIdx.x % LANES;
+        const bool in = i < live * width / 4;
+        const int r = in ? i * 4 / width : 0, word = crank * width + (in ? i * 4 % width : 0);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = from; k < clusters; k += LANES) {
+            const float4 x = __ldcg((const float4 *)(partial + k * stride + r * D + word));
+            const float f = weights[k * R + r];
+            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o *= 2) {
+            v.x += __shfl_xor_sync(~0u, v.x, o), v.y += __shfl_xor_sync(~0u, v.y, o);
+            v.z += __shfl_xor_sync(~0u, v.z, o), v.w += __shfl_xor_sync(~0u, v.w, o);
+        }
+        if (in && from == 0) finish(r, word, v, s_joined[1][r]);
     }
+    if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
 }
 
 template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)
@@ -500,7 +567,7 @@ template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &
     cudaError_t e = allow_smem((const void *)k_kv_attention<D, INT8, NT>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(plan.items * plan.splits));
+    cfg.gridDim = dim3(plan.splits, p.c.kv_heads * plan.row_tiles, p.c.batch);
     cfg.blockDim = dim3(kW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -536,7 +603,7 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     const long long slots = (long long)sm_count() * (plan.tiles8 == 1 ? 3 : 2);
     const long long most = (seen / 16 + kMinBlocks) / kMinBlocks;
     long long splits = plan.items >= slots / 2 ? 4 * slots / plan.items : slots / plan.items;
-    splits = std::max(1ll, std::min(splits, most));
+    splits = std::max(1ll, std::min({splits, most, (long long)kMaxSplits}));
     plan.cluster = splits >= 5 ? 8 : splits >= 3 ? 4 : (int)splits;
     splits = (splits + plan.cluster - 1) / plan.cluster * plan.cluster;
     // without tickets for every item there is one cluster for each
@@ -549,7 +616,8 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
 
 cudaError_t launch_kv_attention(KvAttentionParams p, const KvAttentionPlan &plan, cudaStream_t s)
 {
-    if (plan.items * plan.splits > 0x7fffffff) return cudaErrorInvalidValue;
+    const uint32_t page_blocks = p.c.page_tokens / 16;
+    p.page_magic = page_blocks == 1 ? 0 : (uint32_t)(0xffffffffu / page_blocks) + 1;   // exact below 2^26 blocks of 16
     p.row_tiles = plan.row_tiles;
     p.splits = plan.splits;
     return p.c.dim == 64 ? launch_dim<64>(p, plan, s) : p.c.dim == 128 ? launch_dim<128>(p, plan, s) : launch_dim<256>(p, plan, s);

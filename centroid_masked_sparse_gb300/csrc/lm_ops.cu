@@ -34,6 +34,7 @@ mtp_status check_cache(const mtp_kv_desc *d, const mtp_kv_batch *s)
     if (!s->page_table || !s->lengths) return MTP_ERR_NULL;
     if (s->batch > 65535) return MTP_ERR_UNSUPPORTED;
     if (s->max_tokens < 1 || s->table_width < 1 || s->ld_table < s->table_width) return MTP_ERR_SHAPE;
+    if ((int64_t)s->table_width * d->page_tokens > 1 << 30) return MTP_ERR_UNSUPPORTED;
     if (!s->starts && s->tokens % s->batch != 0) return MTP_ERR_SHAPE;
     if (!aligned(d->k_codes, 16) || !aligned(d->v_codes, 16) || !aligned(d->k_scales, 4) || !aligned(d->v_scales, 4) ||
         !aligned(d->error_word, 4) || !aligned(s->page_table, 4) || !aligned(s->lengths, 4) || !aligned(s->starts, 4))
@@ -210,6 +211,7 @@ mtp_status mtp_kv_attention(const mtp_kv_desc *d, const mtp_kv_batch *seqs, cons
     if (heads < 1 || heads % d->kv_heads != 0 || max_len < 0 || window < 0) return MTP_ERR_SHAPE;
     if (heads > 65535) return MTP_ERR_UNSUPPORTED;
     if (seqs->batch == 0 || seqs->tokens == 0) return MTP_OK;
+    if ((int64_t)(seqs->starts ? seqs->max_tokens : seqs->tokens / seqs->batch) * heads > 1 << 19) return MTP_ERR_UNSUPPORTED;
     if ((st = check_strides(q, q_token_stride, q_head_stride)) != MTP_OK) return st;
     if (!out) return MTP_ERR_NULL;
     if (!workspace || workspace_bytes < MTP_KV_WORKSPACE_ZEROED) return MTP_ERR_WORKSPACE;

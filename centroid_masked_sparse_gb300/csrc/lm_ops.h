@@ -73,6 +73,7 @@ struct KvAttentionParams {
     uint32_t *tickets;       // [items][8], zero between calls
     float *partial;          // sums of the clusters of an item
     int row_tiles, splits;   // set by the plan
+    uint32_t page_magic;     // block / (page_tokens / 16) = umulhi(block, magic), 0: no division
 };
 // How a call is split: CTAs per item (a sequence, a kv head and a tile of query rows), in
 // clusters of `cluster`; the floats that the items' clusters exchange.
@@ -262,6 +263,14 @@ __device__ __forceinline__ float cluster_load(const float *own, uint32_t rank)
     float v;
     asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
                  : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_load4(const float *own, uint32_t rank)
+{
+    const uint32_t addr = (uint32_t)__cvta_generic_to_shared(own);
+    float4 v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
     return v;
 }
 
