@@ -36,18 +36,25 @@ _TYPES = {torch.float32: MTP_TYPE_F32, torch.bfloat16: MTP_TYPE_BF16}
 _FORMATS = {"int8": MTP_KV_INT8, "e4m3": MTP_KV_E4M3}
 
 
+# The current stream's handle by device index; torch.cuda.current_stream takes 2 us to wrap it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _stream(stream, index):
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _vector(t, dtype, n, device):
-    """A contiguous vector of n elements on the call's GPU, or None."""
-    assert t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.device == device)
-    return _ptr(t)
+    """The address of a contiguous tensor of n elements on the call's GPU, or None."""
+    if t is None:
+        return None
+    assert t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.device == device
+    return t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -69,16 +76,16 @@ class Q4Weight:
         assert scales.dim() == 2 and scales.shape[0] == codes.shape[0]
         assert zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
                                  and zeros.device == codes.device)
-        self.device = codes.device
+        self.device, self.index = codes.device, codes.device.index or 0
         self.rows, self.cols = int(codes.shape[0]), 2 * int(codes.shape[1])
         self.group = self.cols // max(1, int(scales.shape[1]))
         assert self.group * int(scales.shape[1]) == self.cols, "scales do not divide the columns into groups"
         size = lib().mtp_q4_packed_bytes(self.rows, self.cols, self.group, zeros is not None)
         self.packed = torch.empty(size, dtype=torch.uint8, device=self.device)
         self.desc = MtpQ4Desc(rows=self.rows, cols=self.cols, group=self.group, zeros=zeros is not None,
-                              device=self.device.index or 0, packed=self.packed.data_ptr(), softcap=0.0)
+                              device=self.index, packed=self.packed.data_ptr(), softcap=0.0)
         check(lib().mtp_q4_pack(ctypes.byref(self.desc), codes.data_ptr(), codes.stride(0) if self.rows > 1 else self.cols // 2,
-                                scales.data_ptr(), _ptr(zeros), self.packed.data_ptr(), size, _stream(stream, self.device)),
+                                scales.data_ptr(), _ptr(zeros), self.packed.data_ptr(), size, _stream(stream, self.index)),
               "mtp_q4_pack")
 
     @classmethod
@@ -96,25 +103,25 @@ def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
     points = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zeros else None
     check(lib().mtp_q4_quantize(w.data_ptr(), w.stride(0) if rows > 1 else cols, rows, cols, group, w.device.index or 0,
                                 codes.data_ptr(), max(1, cols // 2), scales.data_ptr(), _ptr(points),
-                                _stream(stream, w.device)), "mtp_q4_quantize")
+                                _stream(stream, w.device.index or 0)), "mtp_q4_quantize")
     return codes, scales, points
 
 
 def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, stream=None):
     """[B, M]: softcap(x @ w.T) of x bf16 [B, K], in fp32 or rounded once to bf16 (out's type, or out_dtype)."""
-    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == weight.cols and x.stride(1) == 1
-    assert x.device == weight.device
-    batch = int(x.shape[0])
+    batch, cols = x.shape
+    rows = weight.rows
+    assert x.dtype == torch.bfloat16 and cols == weight.cols and x.stride(1) == 1 and x.device == weight.device
     if out is None:
-        out = torch.empty(batch, weight.rows, dtype=out_dtype, device=weight.device)
-    assert out.shape == (batch, weight.rows) and out.stride(1) == 1 and out.device == weight.device
+        out = torch.empty(batch, rows, dtype=out_dtype, device=weight.device)
+    assert out.shape == (batch, rows) and (out.stride(1) == 1 or rows == 1) and out.device == weight.device
     desc = weight.desc
     if softcap != 0.0:
         desc = MtpQ4Desc.from_buffer_copy(desc)
         desc.softcap = softcap
-    check(lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), x.stride(0) if batch > 1 else max(x.stride(0), weight.cols),
-                              batch, out.data_ptr(), _TYPES[out.dtype],
-                              out.stride(0) if batch > 1 else max(out.stride(0), weight.rows), _stream(stream, weight.device)),
+    many = batch > 1
+    check(lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), x.stride(0) if many else cols, batch, out.data_ptr(),
+                              _TYPES[out.dtype], out.stride(0) if many else rows, _stream(stream, weight.index)),
           "mtp_q4_matvec")
     return out
 
@@ -137,12 +144,12 @@ class KvCache:
             assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == k_codes.shape[:2]
         assert len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) == 1
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.format, self.device = format, k_codes.device
+        self.format, self.device, self.index = format, k_codes.device, k_codes.device.index or 0
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = (int(n) for n in k_codes.shape)
         self.errors = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._ws = None
+        self._ws, self._needs = None, {}
         self.desc = MtpKvDesc(num_pages=self.pages, page_tokens=self.page_tokens, kv_heads=self.kv_heads,
-                              head_dim=self.head_dim, format=_FORMATS[format], device=self.device.index or 0,
+                              head_dim=self.head_dim, format=_FORMATS[format], device=self.index,
                               k_codes=k_codes.data_ptr(), v_codes=v_codes.data_ptr(), k_scales=k_scales.data_ptr(),
                               v_scales=v_scales.data_ptr(), error_word=self.errors.data_ptr())
 
@@ -158,10 +165,11 @@ class KvCache:
 
     def workspace(self, need, stream=None):
         """A cached attention workspace of at least `need` bytes, zeroed on the call's stream when it is made."""
-        if self._ws is None or self._ws.numel() < need:
+        ws = self._ws
+        if ws is None or ws.numel() < need:
             with torch.cuda.stream(stream):
-                self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        return self._ws
+                ws = self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return ws
 
     def read_errors(self):
         """The MTP_DEVERR_* bits that the calls so far have set (waits for the GPU), and clears them."""
@@ -171,23 +179,14 @@ class KvCache:
 
 
 def _batch_desc(cache, page_table, lengths, starts, tokens, max_tokens):
-    batch = int(page_table.shape[0])
-    assert page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.device == cache.device
-    assert page_table.stride(1) == 1 or page_table.shape[1] == 1
+    batch, width = page_table.shape
+    device = cache.device
+    assert page_table.dtype == torch.int32 and page_table.device == device and (page_table.stride(1) == 1 or width == 1)
     if max_tokens is None:
         assert starts is None, "ragged calls need the most tokens that one sequence brings"
         max_tokens = max(1, tokens // max(1, batch))
-    width = int(page_table.shape[1])
-    return MtpKvBatch(batch=batch, tokens=tokens, max_tokens=max_tokens, table_width=width,
-                      page_table=page_table.data_ptr(), ld_table=page_table.stride(0) if batch > 1 else width,
-                      lengths=_vector(lengths, torch.int32, batch, cache.device),
-                      starts=_vector(starts, torch.int32, batch + 1, cache.device))
-
-
-def _tokens_ok(cache, t):
-    assert t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[2] == cache.head_dim and t.stride(2) == 1
-    assert t.device == cache.device
-    return t
+    return MtpKvBatch(batch, tokens, max_tokens, width, page_table.data_ptr(), page_table.stride(0) if batch > 1 else width,
+                      _vector(lengths, torch.int32, batch, device), _vector(starts, torch.int32, batch + 1, device))
 
 
 def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, stream=None) -> None:
@@ -195,10 +194,15 @@ def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, s
 
     page_table int32 [B, width], lengths int32 [B]; sequence b brings rows starts[b]..starts[b + 1] (int32
     [B + 1]; at most max_new of them), or without starts an equal share of the rows."""
-    assert _tokens_ok(cache, k).shape == _tokens_ok(cache, v).shape and k.shape[1] == cache.kv_heads
-    seqs = _batch_desc(cache, page_table, lengths, starts, int(k.shape[0]), max_new)
-    check(lib().mtp_kv_append(ctypes.byref(cache.desc), ctypes.byref(seqs), k.data_ptr(), k.stride(0), k.stride(1),
-                              v.data_ptr(), v.stride(0), v.stride(1), _stream(stream, cache.device)), "mtp_kv_append")
+    shape, device = k.shape, cache.device
+    tokens, heads, dim = shape
+    assert heads == cache.kv_heads and dim == cache.head_dim and v.shape == shape
+    assert k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.device == device and v.device == device
+    k_strides, v_strides = k.stride(), v.stride()
+    assert k_strides[2] == 1 and v_strides[2] == 1
+    seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_new)
+    check(lib().mtp_kv_append(ctypes.byref(cache.desc), ctypes.byref(seqs), k.data_ptr(), k_strides[0], k_strides[1],
+                              v.data_ptr(), v_strides[0], v_strides[1], _stream(stream, cache.index)), "mtp_kv_append")
 
 
 def mtp_kv_attention_workspace_bytes(cache, page_table, lengths, tokens, heads, starts=None, max_q=None, max_len=0, window=0) -> int:
@@ -213,22 +217,30 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
     lengths are the tokens of each sequence in the cache, with the ones that q belongs to; starts and max_q as
     in mtp_kv_append; max_len bounds the lengths (0: the table's width); window 0 sees everything; scale is
     head_dim ** -0.5 unless given."""
-    tokens, heads = int(_tokens_ok(cache, q).shape[0]), int(q.shape[1])
+    shape, device = q.shape, cache.device
+    tokens, heads, dim = shape
+    strides = q.stride()
+    assert q.dtype == torch.bfloat16 and dim == cache.head_dim and strides[2] == 1 and q.device == device
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
     if lse is None:
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=cache.device)
-    assert out.dtype == torch.bfloat16 and out.shape == q.shape and out.is_contiguous() and out.device == cache.device
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=device)
+    assert out.shape == shape
     seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_q)
     desc, library = ctypes.byref(cache.desc), lib()
     if workspace is None:
-        workspace = cache.workspace(library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len, window),
-                                    stream)
-    check(library.mtp_kv_attention(desc, ctypes.byref(seqs), q.data_ptr(), q.stride(0), q.stride(1), heads, max_len,
-                                   window, cache.head_dim ** -0.5 if scale is None else scale, out.data_ptr(),
-                                   _vector(lse, torch.float32, tokens * heads, cache.device), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream, cache.device)),
-          "mtp_kv_attention")
+        # what a call needs goes by its sizes
+        key = (seqs.batch, tokens, seqs.max_tokens, seqs.table_width, starts is None, heads, max_len, window)
+        need = cache._needs.get(key)
+        if need is None:
+            if len(cache._needs) > 4096:
+                cache._needs.clear()
+            need = cache._needs[key] = library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len, window)
+        workspace = cache.workspace(need, stream)
+    check(library.mtp_kv_attention(desc, ctypes.byref(seqs), q.data_ptr(), strides[0], strides[1], heads, max_len, window,
+                                   dim ** -0.5 if scale is None else scale, _vector(out, torch.bfloat16, out.numel(), device),
+                                   _vector(lse, torch.float32, tokens * heads, device), workspace.data_ptr(),
+                                   workspace.numel(), _stream(stream, cache.index)), "mtp_kv_attention")
     return out, lse
 
 
@@ -246,34 +258,32 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]
 
 
-def _logits_ok(logits):
-    assert logits.dim() == 2 and logits.dtype in _TYPES
-    assert logits.stride(1) == 1 or logits.shape[1] == 1
-    return int(logits.shape[0]), int(logits.shape[1])
-
-
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+def _rows(t):
+    """Rows, columns and row stride of a matrix with unit inner stride."""
+    rows, cols = t.shape
+    strides = t.stride()
+    assert strides[1] == 1 or cols == 1
+    return rows, cols, strides[0] if rows > 1 else cols
 
 
 def mtp_token_logprobs(logits, tokens, top=0, temperature=1.0, out=None, stream=None) -> TokenLogprobs:
     """Log probability and rank of tokens[r] (int32 [rows]; outside the vocabulary: no token) in logits[r], the
     row's entropy and lse, and its `top` largest alternatives.  out: an earlier result to write into."""
-    rows, vocab = _logits_ok(logits)
+    rows, vocab, ld = _rows(logits)
     device = logits.device
-    if out is None:
-        def empty(*shape, dtype=torch.float32):
-            return torch.empty(*shape, dtype=dtype, device=device)
-        out = TokenLogprobs(empty(rows), empty(rows), empty(rows, dtype=torch.int32), empty(rows),
-                            empty(rows, top, dtype=torch.int32) if top else None, empty(rows, top) if top else None)
     f32, i32 = torch.float32, torch.int32
-    check(lib().mtp_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], _row_stride(logits), rows, vocab,
+    if out is None:
+        def empty(*shape, dtype=f32):
+            return torch.empty(*shape, dtype=dtype, device=device)
+        out = TokenLogprobs(empty(rows), empty(rows), empty(rows, dtype=i32), empty(rows),
+                            empty(rows, top, dtype=i32) if top else None, empty(rows, top) if top else None)
+    logprob, entropy, rank, lse, top_ids, top_logprobs = out
+    check(lib().mtp_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ld, rows, vocab,
                                    _vector(tokens, i32, rows, device), temperature, top,
-                                   _vector(out.logprob, f32, rows, device), _vector(out.entropy, f32, rows, device),
-                                   _vector(out.rank, i32, rows, device), _vector(out.lse, f32, rows, device),
-                                   _vector(out.top_ids, i32, rows * top, device),
-                                   _vector(out.top_logprobs, f32, rows * top, device), device.index or 0,
-                                   _stream(stream, device)), "mtp_token_logprobs")
+                                   _vector(logprob, f32, rows, device), _vector(entropy, f32, rows, device),
+                                   _vector(rank, i32, rows, device), _vector(lse, f32, rows, device),
+                                   _vector(top_ids, i32, rows * top, device), _vector(top_logprobs, f32, rows * top, device),
+                                   device.index, _stream(stream, device.index)), "mtp_token_logprobs")
     return out
 
 
@@ -281,17 +291,17 @@ def mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad
                                 stream=None):
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with respect to the logits, in their
     type.  out may be the logits themselves."""
-    rows, vocab = _logits_ok(logits)
+    rows, vocab, ld = _rows(logits)
     device, f32 = logits.device, torch.float32
     if out is None:
         out = torch.empty(rows, vocab, dtype=logits.dtype, device=device)
-    assert out.shape == logits.shape and out.dtype == logits.dtype and out.device == device
-    assert out.stride(1) == 1 or vocab == 1
+    out_rows, out_cols, ld_out = _rows(out)
+    assert out_rows == rows and out_cols == vocab and out.dtype == logits.dtype and out.device == device
     check(lib().mtp_token_logprobs_backward(
-        logits.data_ptr(), _TYPES[logits.dtype], _row_stride(logits), rows, vocab, _vector(tokens, torch.int32, rows, device),
-        temperature, _vector(lse, f32, rows, device), _vector(entropy, f32, rows, device),
-        _vector(grad_logprob, f32, rows, device), _vector(grad_entropy, f32, rows, device), out.data_ptr(), _row_stride(out),
-        device.index or 0, _stream(stream, device)), "mtp_token_logprobs_backward")
+        logits.data_ptr(), _TYPES[logits.dtype], ld, rows, vocab, _vector(tokens, torch.int32, rows, device), temperature,
+        _vector(lse, f32, rows, device), _vector(entropy, f32, rows, device), _vector(grad_logprob, f32, rows, device),
+        _vector(grad_entropy, f32, rows, device), out.data_ptr(), ld_out, device.index, _stream(stream, device.index)),
+        "mtp_token_logprobs_backward")
     return out
 
 
