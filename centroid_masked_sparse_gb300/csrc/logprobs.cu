@@ -1,5 +1,23 @@
 // Log probabilities of given tokens, entropy and largest alternatives of rows of logits,
 // and the gradient of the former two.
+//
+// k_token_logprobs.  One pass over a row, shared by the CTAs of a cluster.  With c = log2(e)
+// / temperature, a thread keeps s = sum 2^(x c - R) and t = sum 2^(x c - R) (x c - R) of its
+// logits x, where R is the integer above its largest x c: then x c - R is one fused
+// multiply-add with one rounding, R is exact and so are the powers of two that join the
+// threads' sums; ln sum e^x = (R + log2 s) ln 2, entropy = (log2 s - t / s) ln 2.  A row
+// whose largest |x c| is 2^22 or more (all logits at the type's lowest value, say) is read
+// again with its maximum m and terms of (x - m) c.
+//
+// The alternatives: a thread's tile of logits is looked at only if the largest of it, which
+// the sums need anyway, is above the n-th best value so far.  What passes goes into a
+// shared buffer of (logit, id) keys; a full buffer is reduced to its largest 32 by sorted
+// lists of 32 a warp.  Where a tile would overfill the buffer (the first one, or logits that
+// rise along the row) the n-th largest of the threads' best keys is a bound that at most n
+// threads pass.
+//
+// What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
+// logits in one for most), so the comparisons for rank and maximum work on packed pairs.
 #include <algorithm>
 
 #include "lm_ops.h"
@@ -8,139 +26,574 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
+constexpr int kCand = 2048;       // keys of the buffer
+constexpr int kLpCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+constexpr float kFar = 4194304.f; // |x c| from which R would not be exact
 
-template <typename T> __device__ __forceinline__ float logit_value(T v);
-template <> __device__ __forceinline__ float logit_value(float v) { return v; }
-template <> __device__ __forceinline__ float logit_value(uint16_t v) { return bf16_value(v); }
+typedef unsigned long long u64;
+
+__device__ __forceinline__ u64 pair(float a, float b)
+{
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(u64 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c)
+{
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b)
+{
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b)
+{
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A word of logits: one fp32 or two bf16.
+template <bool BF16> struct Logits;
+template <> struct Logits<false> {
+    typedef float type;
+    static constexpr int VEC = 4;
+    static __device__ __forceinline__ uint32_t masked() { return 0xff800000u; }
+    static __device__ __forceinline__ float value(float v) { return v; }
+};
+template <> struct Logits<true> {
+    typedef uint16_t type;
+    static constexpr int VEC = 8;
+    static __device__ __forceinline__ uint32_t masked() { return 0xff80ff80u; }
+    static __device__ __forceinline__ float value(uint16_t v) { return bf16_value(v); }
+};
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Element e of a vector of logits.
+template <bool BF16> __device__ __forceinline__ float element(const uint4 &v, int e)
+{
+    const uint32_t w = BF16 ? (e / 2 == 0 ? v.x : e / 2 == 1 ? v.y : e / 2 == 2 ? v.z : v.w)
+                            : (e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+    return BF16 ? (e % 2 ? bf_hi(w) : bf_lo(w)) : __uint_as_float(w);
+}
+
+// What stands in for lower logits: their terms are 0 all the same, and it keeps 0 * -inf out.
+__device__ __forceinline__ float lowest(float factor) { return -1e30f / fmaxf(factor, 1.f); }
 
 // (larger logit, then lower id) as one unsigned key; 0 for a masked token.
-__device__ __forceinline__ unsigned long long top_key(float v, int id)
+__device__ __forceinline__ u64 top_key(float v, int id) { return v == -INFINITY ? 0ull : argmax_key(v, id); }
+
+// The warp's 32 keys in falling order, and the largest 32 of two such lists.
+__device__ __forceinline__ u64 exchange(u64 v, int lane, int step, bool up)
 {
-    return v == -INFINITY ? 0ull : argmax_key(v, id);
+    const u64 other = __shfl_xor_sync(~0u, v, step);
+    return ((lane & step) != 0) == up ? max(v, other) : min(v, other);
+}
+__device__ __forceinline__ u64 warp_sort(u64 v, int lane)
+{
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2) v = exchange(v, lane, step, size < 32 && (lane & size) != 0);
+    return v;
+}
+__device__ __forceinline__ u64 warp_merge(u64 a, u64 b, int lane)
+{
+    u64 v = max(a, __shfl_sync(~0u, b, 31 - lane));
+#pragma unroll
+    for (int step = 16; step > 0; step /= 2) v = exchange(v, lane, step, false);
+    return v;
 }
 
-// One CTA per row.  Terms are e = 2^d of d = (x - max x) * c, c = log2(e) / temperature, with
-// the maximum subtracted first: x * c may leave fp32's range, and its rounding would grow
-// with x.  s = sum e and t = sum e * d give ln sum and entropy.
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) k_token_logprobs(LogprobParams p)
+struct TopState {
+    u64 cand[kCand];
+    u64 lists[kLpWarps][32];
+    u64 best[32];        // the largest so far, falling
+    int have;            // keys in cand
+    float least;         // the value of the n-th best, or -inf
+};
+
+// The largest 32 of every warp's list, falling, in lists[0] (and for warp 0 the result).
+__device__ __forceinline__ u64 merge_lists(TopState &top, u64 mine, int warp, int lane)
 {
-    __shared__ float s_a[kLpThreads / 32], s_b[kLpThreads / 32];
-    __shared__ int s_n[kLpThreads / 32];
-    __shared__ unsigned long long s_k[kLpThreads / 32];
-    const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    top.lists[warp][lane] = mine;
+#pragma unroll
+    for (int half = kLpWarps / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp < half) top.lists[warp][lane] = mine = warp_merge(mine, top.lists[warp + half][lane], lane);
+    }
+    return mine;
+}
+
+// Takes the buffer's keys into `best`.  Every thread calls it, with the buffer at rest.
+__device__ __forceinline__ void reduce_buffer(TopState &top, int n, int warp, int lane)
+{
+    const int have = top.have;
+    u64 mine = warp == 0 ? top.best[lane] : 0ull;
+    for (int at = warp * 32; at < have; at += kLpThreads)
+        mine = warp_merge(mine, warp_sort(at + lane < have ? top.cand[at + lane] : 0ull, lane), lane);
+    mine = merge_lists(top, mine, warp, lane);
+    if (warp == 0) {
+        top.best[lane] = mine;
+        if (lane == n - 1) top.least = mine ? ord_value((uint32_t)(mine >> 32)) : -INFINITY;
+        if (lane == 0) top.have = 0;
+    }
+    __syncthreads();
+}
+
+struct Sums {
+    float r, s, t, most;   // reference, sums, largest logit
+    int before;            // tokens before the given one
+};
+
+__device__ __forceinline__ void join(Sums &a, const Sums &b)
+{
+    const float r = fmaxf(a.r, b.r), fa = exp2_fast(a.r - r), fb = exp2_fast(b.r - r);
+    a.t = fa * (a.t - (r - a.r) * a.s) + fb * (b.t - (r - b.r) * b.s);
+    a.s = fa * a.s + fb * b.s;
+    a.r = r;
+    a.most = fmaxf(a.most, b.most);
+    a.before += b.before;
+}
+
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams p)
+{
+    typedef Logits<BF16> L;
+    typedef typename L::type T;
+    constexpr int VEC = L::VEC, EACH = VEC * kVecs;   // logits of a vector, of a thread's tile
+    __shared__ Sums s_warp[kLpWarps], s_cta;
+    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState) : 16];
+    TopState &top = *(TopState *)s_top;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int csize = (int)cluster_size(), crank = (int)cluster_rank(), row = blockIdx.x / csize;
     const T *x = (const T *)p.logits + row * p.ld;
     const float c = p.factor * kLog2e;
+    const float low = lowest(p.factor);
+    const uint32_t low2 = bf16_bits(low) * 0x10001u;
+
+    // The row as scalars up to a 16-byte boundary, vectors, and scalars behind the last; the
+    // first CTA takes the scalars before, the last one those behind, and each its vectors.
+    const int head = min(p.vocab, (int)((16 - ((uintptr_t)x & 15)) % 16 / sizeof(T)));
+    const int all = (p.vocab - head) / VEC, tail = head + all * VEC;
+    const int v_lo = (int)((long long)all * crank / csize), vecs = (int)((long long)all * (crank + 1) / csize) - v_lo;
+    const T *base = x + head + (long long)v_lo * VEC;
+    const int id0 = head + v_lo * VEC;
+    auto load = [&](int tile, uint4 (&v)[kVecs]) {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = (tile * kVecs + j) * kLpThreads + threadIdx.x;
+            v[j] = i < vecs ? ld_stream16((const uint4 *)base + i) : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
+        }
+    };
+    uint4 next[kVecs];
+    load(0, next);
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     const bool has = given >= 0 && given < p.vocab;
-    const float mine = has ? logit_value(x[given]) : 0.f;
+    const float mine = has ? L::value(x[given]) : 0.f;
+    if (TOP) {
+        if (threadIdx.x < 32) top.best[threadIdx.x] = 0;
+        if (threadIdx.x == 0) top.have = 0, top.least = -INFINITY;
+        __syncthreads();
+    }
 
-    float top = -INFINITY;
+    float r = -kFar, most = -INFINITY;
+    u64 s2 = 0, t2 = 0;   // pairs of sums
     int before = 0;
-    for (int i = threadIdx.x; i < p.vocab; i += kLpThreads) {
-        const float v = logit_value(x[i]);
-        top = fmaxf(top, v);
-        before += v > mine || (v == mine && i < given);
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        before += __shfl_xor_sync(~0u, before, o);
-    }
-    if (lane == 0) s_a[warp] = top, s_n[warp] = before;
-    __syncthreads();
-    before = 0;
-    for (int w = 0; w < kLpThreads / 32; ++w) top = fmaxf(top, s_a[w]), before += s_n[w];
-    __syncthreads();
-    const float m = top == -INFINITY ? 0.f : top;
-    float s = 0.f, t = 0.f;
-    for (int i = threadIdx.x; i < p.vocab; i += kLpThreads) {
-        const float d = (logit_value(x[i]) - m) * c, e = exp2_fast(d);
-        s += e;
-        if (e > 0.f) t = fmaf(e, d, t);
-    }
-    s = warp_sum(s), t = warp_sum(t);
-    if (lane == 0) s_a[warp] = s, s_b[warp] = t;
-    __syncthreads();
-    s = t = 0.f;
-    for (int w = 0; w < kLpThreads / 32; ++w) s += s_a[w], t += s_b[w];
-    const float lns = logf(s);
-    if (threadIdx.x == 0) {
-        if (p.lse) p.lse[row] = fmaf(m, p.factor, lns);
-        if (p.entropy) p.entropy[row] = s == 0.f ? 0.f : lns - t / s * kLn2;
-        if (p.logprob)
-            p.logprob[row] = !has ? 0.f : mine == -INFINITY ? -INFINITY + s * 0.f : fmaf(mine - m, p.factor, -lns);
-        if (p.rank) p.rank[row] = has ? before : -1;
-    }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < p.top; ++k) {
-        unsigned long long best = 0;
-        for (int i = threadIdx.x; i < p.vocab; i += kLpThreads) {
-            const unsigned long long key = top_key(logit_value(x[i]), i);
-            if (key < last && key > best) best = key;
+    auto raise = [&](float to) {   // the reference is at least `to` from here on
+        const float up = ceilf(to);
+        if (up > r) {
+            const float f = exp2_fast(r - up), d = up - r;
+            s2 = mul2(s2, pair(f, f));
+            t2 = fma2(t2, pair(f, f), mul2(s2, pair(-d, -d)));
+            r = up;
         }
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
+    };
+    auto add = [&](float a, float b) {   // two logits, or one and -inf
+        const u64 d = fma2(pair(a, b), pair(c, c), pair(-r, -r));
+        const float2 u = unpair(d);
+        const u64 e = pair(exp2_fast(u.x), exp2_fast(u.y));
+        s2 = add2(s2, e);
+        t2 = fma2(e, d, t2);
+    };
+    auto one = [&](int id) {   // a scalar before or behind the vectors
+        const float v = L::value(x[id]);
+        most = fmaxf(most, v);
+        raise(v * c);
+        add(max_nan(v, low), low);
+        before += v > mine || (v == mine && id < given);
+        if (TOP && v > -INFINITY) top.cand[atomicAdd(&top.have, 1)] = top_key(v, id);
+    };
+    if (crank == 0 && threadIdx.x < head) one(threadIdx.x);
+    if (TOP) __syncthreads();
+
+    const int tiles = (vecs + kVecs * kLpThreads - 1) / (kVecs * kLpThreads);
+    for (int tile = 0; tile < tiles; ++tile) {
+        uint4 v[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) v[j] = next[j];
+        load(tile + 1, next);
+        const int first = id0 + tile * kVecs * kLpThreads * VEC;   // the tile's ids
+        const int have = TOP ? top.have : 0;
+        const float least = TOP ? top.least : 0.f;
+
+        float high;   // the thread's largest of the tile
+        if (BF16) {
+            uint32_t m = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
+#pragma unroll
+            for (int j = 1; j < kVecs; ++j) m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w)));
+            high = fmaxf(bf_lo(m), bf_hi(m));
+        } else {
+            high = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) high = fmaxf(high, element<BF16>(v[j], e));
+        }
+        most = fmaxf(most, high);
+        raise(high * c);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            if (BF16) {
+                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = max_nan_bf16x2(w[i], low2);
+                    add(bf_lo(u), bf_hi(u));
+                }
+            } else {
+                add(max_nan(__uint_as_float(v[j].x), low), max_nan(__uint_as_float(v[j].y), low));
+                add(max_nan(__uint_as_float(v[j].z), low), max_nan(__uint_as_float(v[j].w), low));
+            }
+        }
+
+        if (p.rank && has) {
+            // logits that come before the given one: not below it at lower ids, above it at
+            // higher ones
+            // (a masked one would count what stands in for logits behind the last)
+            const long long last = first + (long long)kVecs * kLpThreads * VEC;
+            if ((first <= given && given < last) || mine == -INFINITY) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int id = first + (j * kLpThreads + threadIdx.x) * VEC + e;
+                        const float u = element<BF16>(v[j], e);
+                        before += (tile * kVecs + j) * kLpThreads + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
+                    }
+            } else if (BF16) {
+                const uint32_t m = bf16_bits(mine) * 0x10001u;
+                uint32_t count = 0;   // as bf16, at most 16 each
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t is;
+                        if (given >= last)
+                            asm("set.ge.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
+                        else
+                            asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
+                        asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(is));
+                    }
+                }
+                before += (int)bf_lo(count) + (int)bf_hi(count);
+            } else if (given >= last) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) >= mine;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) > mine;
+            }
+        }
+
+        if (TOP) {
+            // later tiles have higher ids, so that an equal value does not pass
+            const bool pass = high > least;
+            const int passing = __syncthreads_count(pass);
+            if (passing == 0) continue;
+            u64 bound = 0;
+            if (have + passing * EACH > kCand) {
+                u64 key = 0;
+                if (pass)
+#pragma unroll
+                    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (element<BF16>(v[j], e) == high)
+                                key = max(key, top_key(high, first + (j * kLpThreads + threadIdx.x) * VEC + e));
+                merge_lists(top, warp_sort(key, lane), warp, lane);
+                __syncthreads();
+                bound = top.lists[0][p.top - 1];
+            }
+            if (pass)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float u = element<BF16>(v[j], e);
+                        if (u > least) {
+                            const u64 key = top_key(u, first + (j * kLpThreads + threadIdx.x) * VEC + e);
+                            if (key >= bound) top.cand[atomicAdd(&top.have, 1)] = key;
+                        }
+                    }
+            __syncthreads();
+            if (top.have > kCand / 2) reduce_buffer(top, p.top, warp, lane);
+        }
+    }
+    if (TOP) __syncthreads();   // every thread has decided on the buffer of the last tile
+    if (crank == csize - 1 && threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
+    if (TOP) {
         __syncthreads();
-        if (lane == 0) s_k[warp] = best;
+        reduce_buffer(top, p.top, warp, lane);
+    }
+
+    // join the threads, the warps, the cluster
+    auto join_all = [&](Sums a) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            Sums b;
+            b.r = __shfl_xor_sync(~0u, a.r, o), b.s = __shfl_xor_sync(~0u, a.s, o), b.t = __shfl_xor_sync(~0u, a.t, o);
+            b.most = __shfl_xor_sync(~0u, a.most, o), b.before = __shfl_xor_sync(~0u, a.before, o);
+            join(a, b);
+        }
+        if (lane == 0) s_warp[warp] = a;
         __syncthreads();
-        for (int w = 0; w < kLpThreads / 32; ++w) best = max(best, s_k[w]);
-        last = best;
-        if (threadIdx.x == 0) {
+        a = s_warp[0];
+#pragma unroll
+        for (int w = 1; w < kLpWarps; ++w) join(a, s_warp[w]);
+        if (csize > 1) {
+            if (threadIdx.x == 0) s_cta = a;
+            cluster_sync();
+            for (int k = 0; k < csize; ++k) {
+                Sums b;
+                b.r = cluster_load(&s_cta.r, k), b.s = cluster_load(&s_cta.s, k), b.t = cluster_load(&s_cta.t, k);
+                b.most = cluster_load(&s_cta.most, k), b.before = __float_as_int(cluster_load((const float *)&s_cta.before, k));
+                if (k == 0)
+                    a = b;
+                else
+                    join(a, b);
+            }
+        }
+        return a;
+    };
+    const float2 s1 = unpair(s2), t1 = unpair(t2);
+    Sums sums = join_all(Sums{r, s1.x + s1.y, t1.x + t1.y, most, before});
+    const bool far = fabsf(sums.most * c) >= kFar && fabsf(sums.most) < INFINITY;
+    if (far) {
+        // once more, with the maximum
+        const float m = sums.most;
+        float s = 0.f, t = 0.f;
+        auto term = [&](float v) {
+            const float d = max_nan((v - m) * c, -200.f), e = exp2_fast(d);
+            s += e, t = fmaf(e, d, t);
+        };
+        if (crank == 0 && threadIdx.x < head) term(L::value(x[threadIdx.x]));
+        if (crank == csize - 1 && threadIdx.x < p.vocab - tail) term(L::value(x[tail + threadIdx.x]));
+        for (int i = threadIdx.x; i < vecs * VEC; i += kLpThreads) term(L::value(base[i]));
+        if (csize > 1) cluster_sync();   // the sums have been read
+        __syncthreads();
+        const int rank = sums.before;
+        sums = join_all(Sums{0.f, s, t, m, 0});
+        sums.before = rank;
+    }
+    if (csize > 1 && TOP && crank == 0 && warp == 0) {
+        u64 best = top.best[lane];
+        for (int k = 1; k < csize; ++k) {
+            const float *other = (const float *)&top.best[lane];
+            const u64 key = (u64)__float_as_uint(cluster_load(other, k)) | (u64)__float_as_uint(cluster_load(other + 1, k)) << 32;
+            best = warp_merge(best, key, lane);
+        }
+        top.best[lane] = best;
+    }
+    if (crank == 0 && warp == 0) {
+        // a row that holds a NaN has a NaN in s, one with a +inf gets it here
+        const float s = sums.most == INFINITY ? sums.s - sums.s + NAN : sums.s;
+        const float ln_s = logf(s), log2_s = log2f(s);
+        auto logprob = [&](float v) {
+            if (v == -INFINITY) return -INFINITY + s * 0.f;
+            if (far) return fmaf(v - sums.most, p.factor, -ln_s);
+            if (v * c < -kFar) return fmaf(v, p.factor, -(sums.r + log2_s) * kLn2);   // v c may leave fp32's range
+            return (fmaf(v, c, -sums.r) - log2_s) * kLn2;
+        };
+        if (lane == 0) {
+            if (p.lse) p.lse[row] = far ? fmaf(sums.most, p.factor, ln_s) : (sums.r + log2_s) * kLn2;
+            if (p.entropy) p.entropy[row] = s == 0.f ? 0.f : (log2_s - sums.t / s) * kLn2;
+            if (p.logprob) p.logprob[row] = has ? logprob(mine) : 0.f;
+            if (p.rank) p.rank[row] = has ? sums.before : -1;
+        }
+        if (TOP && lane < p.top) {
             int id;
             float v;
-            decode_argmax_key(best, &id, &v);
-            p.top_ids[(long long)row * p.top + k] = id;
-            if (p.top_logprobs)
-                p.top_logprobs[(long long)row * p.top + k] = best == 0 ? -INFINITY + s * 0.f : fmaf(v - m, p.factor, -lns);
+            decode_argmax_key(top.best[lane], &id, &v);
+            p.top_ids[(long long)row * p.top + lane] = id;
+            if (p.top_logprobs) p.top_logprobs[(long long)row * p.top + lane] = logprob(v);
         }
     }
+    if (csize > 1) cluster_sync();   // the first CTA may still be reading the others' lists
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) k_token_logprobs_backward(LogprobGradParams p)
+// grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))).  The logit of a masked
+// token is replaced by `low`, whose p is 0.
+constexpr int kGradVecs = 4;   // vectors of a thread
+
+template <bool BF16> __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_backward(LogprobGradParams p)
 {
+    typedef Logits<BF16> L;
+    typedef typename L::type T;
+    constexpr int VEC = L::VEC;
     const int row = blockIdx.x;
     const T *x = (const T *)p.logits + row * p.ld;
     T *g = (T *)p.grad + row * p.ld_grad;
-    const float lse = __ldg(p.lse + row);
+    const int head = min(p.vocab, (int)((16 - ((uintptr_t)x & 15)) % 16 / sizeof(T)));
+    const int vecs = (p.vocab - head) / VEC, tail = head + vecs * VEC;
+    const float low = lowest(p.factor);
+    const uint32_t low2 = bf16_bits(low) * 0x10001u;
+    const bool together = (((uintptr_t)x ^ (uintptr_t)g) & 15) == 0;   // both on 16-byte boundaries at once
+    const float lse_in = __ldg(p.lse + row), lse = lse_in == -INFINITY ? 0.f : lse_in;   // nothing but masked tokens: all 0
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
-    const bool has = given >= 0 && given < p.vocab;
-    const float gl = p.grad_logprob && has ? __ldg(p.grad_logprob + row) : 0.f;
-    const float ge = p.grad_entropy ? __ldg(p.grad_entropy + row) : 0.f;
-    const float h = p.grad_entropy ? __ldg(p.entropy + row) : 0.f;
-    for (long long i = blockIdx.y * kLpThreads + threadIdx.x; i < p.vocab; i += gridDim.y * kLpThreads) {
-        const float v = logit_value(x[i]);
-        float r = 0.f;
-        if (v != -INFINITY) {
-            const float d = fmaf(v, p.factor, -lse), e = exp2_fast(d * kLog2e);
-            r = ((i == given ? gl : 0.f) - e * (gl + ge * (d + h))) * p.factor;
-        }
-        if constexpr (sizeof(T) == 2)
-            g[i] = bf16_bits(r);
+    const float hot = p.grad_logprob && given >= 0 && given < p.vocab ? __ldg(p.grad_logprob + row) * p.factor : 0.f;
+    const float ge = p.grad_entropy ? -__ldg(p.grad_entropy + row) * p.factor : 0.f;
+    const float gl = (p.grad_entropy ? ge * __ldg(p.entropy + row) : 0.f) - hot;
+    auto pair_of = [&](float a, float b) {   // the gradient of two logits, the given one's 1 apart
+        const u64 d = fma2(pair(a, b), pair(p.factor, p.factor), pair(-lse, -lse));
+        const float2 e = unpair(mul2(d, pair(kLog2e, kLog2e)));
+        return mul2(pair(exp2_fast(e.x), exp2_fast(e.y)), fma2(d, pair(ge, ge), pair(gl, gl)));
+    };
+    auto put = [&](T *to, float v) {
+        if constexpr (BF16)
+            *to = bf16_bits(v);
         else
-            g[i] = r;
+            *to = v;
+    };
+    auto one = [&](int i) {
+        const float v = L::value(x[i]);
+        float r = unpair(pair_of(max_nan(v, low), 0.f)).x;
+        if (i == given && v != -INFINITY) r += hot;
+        put(g + i, r);
+    };
+    if (blockIdx.y == 0) {
+        if (threadIdx.x < head) one(threadIdx.x);
+        if (threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
     }
+    for (int v0 = blockIdx.y * kGradVecs * kLpThreads; v0 < vecs; v0 += gridDim.y * kGradVecs * kLpThreads) {
+        uint4 in[kGradVecs];
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+            const int i = v0 + j * kLpThreads + threadIdx.x;
+            if (i < vecs) in[j] = __ldcs((const uint4 *)(x + head) + i);
+        }
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+            const int i = v0 + j * kLpThreads + threadIdx.x, id = head + i * VEC;
+            if (i >= vecs) break;
+            float r[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) {
+                float2 u;
+                if (BF16) {
+                    const uint32_t w = max_nan_bf16x2(e == 0 ? in[j].x : e == 2 ? in[j].y : e == 4 ? in[j].z : in[j].w, low2);
+                    u = unpair(pair_of(bf_lo(w), bf_hi(w)));
+                } else {
+                    u = unpair(pair_of(max_nan(element<BF16>(in[j], e), low), max_nan(element<BF16>(in[j], e + 1), low)));
+                }
+                r[e] = u.x, r[e + 1] = u.y;
+            }
+            if (given >= id && given < id + VEC) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (id + e == given && element<BF16>(in[j], e) != -INFINITY) r[e] += hot;
+            }
+            if (together) {
+                uint4 out;
+                if (BF16) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(r[(2 * e + 1) % VEC]), "f"(r[2 * e % VEC]));
+                    out = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    out = make_uint4(__float_as_uint(r[0]), __float_as_uint(r[1]), __float_as_uint(r[2]), __float_as_uint(r[3]));
+                }
+                __stcs((uint4 *)(g + id), out);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) put(g + id + e, r[e]);
+            }
+        }
+    }
+}
+
+template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &p, int cluster, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.rows * cluster);
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobParams &p, bool bf16, cudaStream_t s)
 {
-    if (bf16)
-        k_token_logprobs<uint16_t><<<p.rows, kLpThreads, 0, s>>>(p);
-    else
-        k_token_logprobs<float><<<p.rows, kLpThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    // CTAs of a row: enough for several rounds over the GPU, each with at least a tile
+    const long long tile = (long long)kLpThreads * kVecs * (bf16 ? 8 : 4), slots = 3ll * sm_count();
+    int cluster = 1;
+    while (cluster < kLpCluster && p.rows * cluster < 3 * slots && p.vocab >= 2 * cluster * tile) cluster *= 2;
+    if (bf16) return p.top ? launch_logprobs<true, true>(p, cluster, s) : launch_logprobs<true, false>(p, cluster, s);
+    return p.top ? launch_logprobs<false, true>(p, cluster, s) : launch_logprobs<false, false>(p, cluster, s);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams &p, bool bf16, cudaStream_t s)
 {
-    const dim3 grid(p.rows, (unsigned)std::min((p.vocab + kLpThreads * 16ll - 1) / (kLpThreads * 16), 65535ll));
+    const long long each = (long long)kLpThreads * kGradVecs * (bf16 ? 8 : 4);
+    const dim3 grid(p.rows, (unsigned)std::min((p.vocab + each - 1) / each, 65535ll));
     if (bf16)
-        k_token_logprobs_backward<uint16_t><<<grid, kLpThreads, 0, s>>>(p);
+        k_token_logprobs_backward<true><<<grid, kLpThreads, 0, s>>>(p);
     else
-        k_token_logprobs_backward<float><<<grid, kLpThreads, 0, s>>>(p);
+        k_token_logprobs_backward<false><<<grid, kLpThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
