@@ -26,10 +26,9 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
 constexpr int kCand = 2048;       // keys of the buffer
-constexpr int kLpCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kFar = 4194304.f; // |x c| from which R would not be exact
 
@@ -115,12 +114,12 @@ __device__ __forceinline__ float lowest(float factor) { return -1e30f / fmaxf(fa
 __device__ __forceinline__ u64 top_key(float v, int id) { return v == -INFINITY ? 0ull : argmax_key(v, id); }
 
 // The warp's 32 keys in falling order, and the largest 32 of two such lists.
-__device__ __forceinline__ u64 exchange(u64 v, int lane, int step, bool up)
+template <typename K> __device__ __forceinline__ K exchange(K v, int lane, int step, bool up)
 {
-    const u64 other = __shfl_xor_sync(~0u, v, step);
+    const K other = __shfl_xor_sync(~0u, v, step);
     return ((lane & step) != 0) == up ? max(v, other) : min(v, other);
 }
-__device__ __forceinline__ u64 warp_sort(u64 v, int lane)
+template <typename K> __device__ __forceinline__ K warp_sort(K v, int lane)
 {
 #pragma unroll
     for (int size = 2; size <= 32; size *= 2)
@@ -128,42 +127,42 @@ __device__ __forceinline__ u64 warp_sort(u64 v, int lane)
         for (int step = size / 2; step > 0; step /= 2) v = exchange(v, lane, step, size < 32 && (lane & size) != 0);
     return v;
 }
-__device__ __forceinline__ u64 warp_merge(u64 a, u64 b, int lane)
+template <typename K> __device__ __forceinline__ K warp_merge(K a, K b, int lane)
 {
-    u64 v = max(a, __shfl_sync(~0u, b, 31 - lane));
+    K v = max(a, __shfl_sync(~0u, b, 31 - lane));
 #pragma unroll
     for (int step = 16; step > 0; step /= 2) v = exchange(v, lane, step, false);
     return v;
 }
 
-struct TopState {
+template <int W> struct TopState {
     u64 cand[kCand];
-    u64 lists[kLpWarps][32];
+    u64 lists[W][32];
     u64 best[32];        // the largest so far, falling
     int have;            // keys in cand
     float least;         // the value of the n-th best, or -inf
 };
 
-// The largest 32 of every warp's list, falling, in lists[0] (and for warp 0 the result).
-__device__ __forceinline__ u64 merge_lists(TopState &top, u64 mine, int warp, int lane)
+// The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
+template <int W, typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K mine, int warp, int lane)
 {
-    top.lists[warp][lane] = mine;
+    lists[warp][lane] = mine;
 #pragma unroll
-    for (int half = kLpWarps / 2; half > 0; half /= 2) {
+    for (int half = W / 2; half > 0; half /= 2) {
         __syncthreads();
-        if (warp < half) top.lists[warp][lane] = mine = warp_merge(mine, top.lists[warp + half][lane], lane);
+        if (warp < half) lists[warp][lane] = mine = warp_merge(mine, lists[warp + half][lane], lane);
     }
     return mine;
 }
 
 // Takes the buffer's keys into `best`.  Every thread calls it, with the buffer at rest.
-__device__ __forceinline__ void reduce_buffer(TopState &top, int n, int warp, int lane)
+template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top, int n, int warp, int lane)
 {
     const int have = top.have;
     u64 mine = warp == 0 ? top.best[lane] : 0ull;
-    for (int at = warp * 32; at < have; at += kLpThreads)
+    for (int at = warp * 32; at < have; at += W * 32)
         mine = warp_merge(mine, warp_sort(at + lane < have ? top.cand[at + lane] : 0ull, lane), lane);
-    mine = merge_lists(top, mine, warp, lane);
+    mine = merge_lists<W>(top.lists, mine, warp, lane);
     if (warp == 0) {
         top.best[lane] = mine;
         if (lane == n - 1) top.least = mine ? ord_value((uint32_t)(mine >> 32)) : -INFINITY;
@@ -173,29 +172,34 @@ __device__ __forceinline__ void reduce_buffer(TopState &top, int n, int warp, in
 }
 
 struct Sums {
-    float r, s, t, most;   // reference, sums, largest logit
+    float r, s, t, most;   // reference (an integer, or 0 for all), sums, largest logit
     int before;            // tokens before the given one
 };
 
-__device__ __forceinline__ void join(Sums &a, const Sums &b)
+// The warp's sums, in every lane.
+__device__ __forceinline__ Sums warp_join(Sums a)
 {
-    const float r = fmaxf(a.r, b.r), fa = exp2_fast(a.r - r), fb = exp2_fast(b.r - r);
-    a.t = fa * (a.t - (r - a.r) * a.s) + fb * (b.t - (r - b.r) * b.s);
-    a.s = fa * a.s + fb * b.s;
-    a.r = r;
-    a.most = fmaxf(a.most, b.most);
-    a.before += b.before;
+    Sums j;
+    // references below +-kFar are integers; one beyond makes the row's second reading, or a NaN
+    const int r = (int)fminf(fmaxf(a.r, -2.f * kFar), 2.f * kFar), top = __reduce_max_sync(~0u, r);
+    const float f = exp2_fast((float)(r - top));
+    j.r = (float)top;
+    j.s = warp_sum(f * a.s);
+    j.t = warp_sum(f * fmaf((float)(r - top), a.s, a.t));
+    j.most = ord_value(__reduce_max_sync(~0u, ord_key(a.most)));
+    j.before = __reduce_add_sync(~0u, a.before);
+    return j;
 }
 
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams p)
+template <bool BF16, bool TOP, int W>
+__global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
-    constexpr int VEC = L::VEC, EACH = VEC * kVecs;   // logits of a vector, of a thread's tile
-    __shared__ Sums s_warp[kLpWarps], s_cta;
-    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState) : 16];
-    TopState &top = *(TopState *)s_top;
+    constexpr int TH = W * 32, VEC = L::VEC, EACH = VEC * kVecs;   // threads; logits of a vector, of a thread's tile
+    __shared__ Sums s_warp[W], s_cta, s_row;
+    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState<W>) : 16];
+    TopState<W> &top = *(TopState<W> *)s_top;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int csize = (int)cluster_size(), crank = (int)cluster_rank(), row = blockIdx.x / csize;
     const T *x = (const T *)p.logits + row * p.ld;
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
     auto load = [&](int tile, uint4 (&v)[kVecs]) {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int i = (tile * kVecs + j) * kLpThreads + threadIdx.x;
+            const int i = (tile * kVecs + j) * TH + threadIdx.x;
             v[j] = i < vecs ? ld_stream16((const uint4 *)base + i) : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
         }
     };
@@ -240,46 +244,46 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
             r = up;
         }
     };
-    auto add = [&](float a, float b) {   // two logits, or one and -inf
+    auto add = [&](float a, float b) {   // two logits, or one and `low`
         const u64 d = fma2(pair(a, b), pair(c, c), pair(-r, -r));
         const float2 u = unpair(d);
         const u64 e = pair(exp2_fast(u.x), exp2_fast(u.y));
         s2 = add2(s2, e);
         t2 = fma2(e, d, t2);
     };
+    auto push = [&](u64 key) { top.cand[atomicAdd(&top.have, 1)] = key; };
     auto one = [&](int id) {   // a scalar before or behind the vectors
         const float v = L::value(x[id]);
         most = fmaxf(most, v);
         raise(v * c);
         add(max_nan(v, low), low);
         before += v > mine || (v == mine && id < given);
-        if (TOP && v > -INFINITY) top.cand[atomicAdd(&top.have, 1)] = top_key(v, id);
+        if (TOP && v > -INFINITY) push(top_key(v, id));
     };
     if (crank == 0 && threadIdx.x < head) one(threadIdx.x);
     if (TOP) __syncthreads();
 
-    const int tiles = (vecs + kVecs * kLpThreads - 1) / (kVecs * kLpThreads);
+    const int tiles = (vecs + kVecs * TH - 1) / (kVecs * TH);
     for (int tile = 0; tile < tiles; ++tile) {
         uint4 v[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) v[j] = next[j];
         load(tile + 1, next);
-        const int first = id0 + tile * kVecs * kLpThreads * VEC;   // the tile's ids
+        const int first = id0 + tile * kVecs * TH * VEC;   // the tile's ids
         const int have = TOP ? top.have : 0;
         const float least = TOP ? top.least : 0.f;
 
-        float high;   // the thread's largest of the tile
-        if (BF16) {
-            uint32_t m = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
+        float high_of[kVecs], high;   // the thread's largest of each vector, and of the tile
 #pragma unroll
-            for (int j = 1; j < kVecs; ++j) m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w)));
-            high = fmaxf(bf_lo(m), bf_hi(m));
-        } else {
-            high = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) high = fmaxf(high, element<BF16>(v[j], e));
+        for (int j = 0; j < kVecs; ++j) {
+            if (BF16) {
+                const uint32_t m = max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w));
+                high_of[j] = fmaxf(bf_lo(m), bf_hi(m));
+            } else {
+                high_of[j] = fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
+                                   fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w)));
+            }
+            high = j ? fmaxf(high, high_of[j]) : high_of[j];
         }
         most = fmaxf(most, high);
         raise(high * c);
@@ -300,17 +304,16 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
 
         if (p.rank && has) {
             // logits that come before the given one: not below it at lower ids, above it at
-            // higher ones
-            // (a masked one would count what stands in for logits behind the last)
-            const long long last = first + (long long)kVecs * kLpThreads * VEC;
+            // higher ones (a masked one would count what stands in for logits behind the last)
+            const long long last = first + (long long)kVecs * TH * VEC;
             if ((first <= given && given < last) || mine == -INFINITY) {
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const int id = first + (j * kLpThreads + threadIdx.x) * VEC + e;
+                        const int id = first + (j * TH + threadIdx.x) * VEC + e;
                         const float u = element<BF16>(v[j], e);
-                        before += (tile * kVecs + j) * kLpThreads + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
+                        before += (tile * kVecs + j) * TH + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
                     }
             } else if (BF16) {
                 const uint32_t m = bf16_bits(mine) * 0x10001u;
@@ -347,31 +350,44 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
             const bool pass = high > least;
             const int passing = __syncthreads_count(pass);
             if (passing == 0) continue;
-            u64 bound = 0;
+            float bound = least;   // what passes is above `least` and not below `bound`,
+            u64 key_bound = 0;     // its key not below `key_bound`
             if (have + passing * EACH > kCand) {
-                u64 key = 0;
-                if (pass)
-#pragma unroll
-                    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (element<BF16>(v[j], e) == high)
-                                key = max(key, top_key(high, first + (j * kLpThreads + threadIdx.x) * VEC + e));
-                merge_lists(top, warp_sort(key, lane), warp, lane);
+                // the n-th largest of the threads' best values; with ties in it, of their keys
+                const uint32_t mark = pass ? ord_key(high) : 0u;
+                uint32_t(*lists)[32] = (uint32_t(*)[32])top.lists;
+                merge_lists<W>(lists, warp_sort(mark, lane), warp, lane);
                 __syncthreads();
-                bound = top.lists[0][p.top - 1];
+                const uint32_t nth = lists[0][p.top - 1];
+                bound = ord_value(nth);
+                if (have + __syncthreads_count(mark >= nth) * EACH > kCand) {
+                    u64 key = 0;
+                    if (pass)
+#pragma unroll
+                        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                            for (int e = 0; e < VEC; ++e)
+                                if (element<BF16>(v[j], e) == high)
+                                    key = max(key, top_key(high, first + (j * TH + threadIdx.x) * VEC + e));
+                    merge_lists<W>(top.lists, warp_sort(key, lane), warp, lane);
+                    __syncthreads();
+                    key_bound = top.lists[0][p.top - 1];
+                }
             }
-            if (pass)
+            if (pass && high >= bound)
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
+                    if (high_of[j] > least && high_of[j] >= bound)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float u = element<BF16>(v[j], e);
-                        if (u > least) {
-                            const u64 key = top_key(u, first + (j * kLpThreads + threadIdx.x) * VEC + e);
-                            if (key >= bound) top.cand[atomicAdd(&top.have, 1)] = key;
+                        for (int e = 0; e < VEC; ++e) {
+                            const float u = element<BF16>(v[j], e);
+                            if (u > least && u >= bound) {
+                                const u64 key = top_key(u, first + (j * TH + threadIdx.x) * VEC + e);
+                                if (key >= key_bound) push(key);
+                            }
                         }
-                    }
+            // n values at the bound or above it are in the buffer now
+            if (bound > least && threadIdx.x == 0) top.least = bound;
             __syncthreads();
             if (top.have > kCand / 2) reduce_buffer(top, p.top, warp, lane);
         }
@@ -383,34 +399,30 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
         reduce_buffer(top, p.top, warp, lane);
     }
 
-    // join the threads, the warps, the cluster
+    // join the threads, the warps (by warp 0), the cluster (by every CTA's warp 0)
     auto join_all = [&](Sums a) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Sums b;
-            b.r = __shfl_xor_sync(~0u, a.r, o), b.s = __shfl_xor_sync(~0u, a.s, o), b.t = __shfl_xor_sync(~0u, a.t, o);
-            b.most = __shfl_xor_sync(~0u, a.most, o), b.before = __shfl_xor_sync(~0u, a.before, o);
-            join(a, b);
-        }
+        a = warp_join(a);
         if (lane == 0) s_warp[warp] = a;
         __syncthreads();
-        a = s_warp[0];
-#pragma unroll
-        for (int w = 1; w < kLpWarps; ++w) join(a, s_warp[w]);
+        if (warp == 0) {
+            const Sums none = {-2.f * kFar, 0.f, 0.f, -INFINITY, 0};
+            a = warp_join(lane < W ? s_warp[lane] : none);
+            if (lane == 0) s_cta = a, s_row = a;
+        }
         if (csize > 1) {
-            if (threadIdx.x == 0) s_cta = a;
             cluster_sync();
-            for (int k = 0; k < csize; ++k) {
-                Sums b;
-                b.r = cluster_load(&s_cta.r, k), b.s = cluster_load(&s_cta.s, k), b.t = cluster_load(&s_cta.t, k);
-                b.most = cluster_load(&s_cta.most, k), b.before = __float_as_int(cluster_load((const float *)&s_cta.before, k));
-                if (k == 0)
-                    a = b;
-                else
-                    join(a, b);
+            if (warp == 0) {
+                Sums b = {-2.f * kFar, 0.f, 0.f, -INFINITY, 0};
+                if (lane < csize) {
+                    b.r = cluster_load(&s_cta.r, lane), b.s = cluster_load(&s_cta.s, lane), b.t = cluster_load(&s_cta.t, lane);
+                    b.most = cluster_load(&s_cta.most, lane), b.before = __float_as_int(cluster_load((const float *)&s_cta.before, lane));
+                }
+                b = warp_join(b);
+                if (lane == 0) s_row = b;
             }
         }
-        return a;
+        __syncthreads();
+        return s_row;
     };
     const float2 s1 = unpair(s2), t1 = unpair(t2);
     Sums sums = join_all(Sums{r, s1.x + s1.y, t1.x + t1.y, most, before});
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
         };
         if (crank == 0 && threadIdx.x < head) term(L::value(x[threadIdx.x]));
         if (crank == csize - 1 && threadIdx.x < p.vocab - tail) term(L::value(x[tail + threadIdx.x]));
-        for (int i = threadIdx.x; i < vecs * VEC; i += kLpThreads) term(L::value(base[i]));
+        for (long long i = threadIdx.x; i < (long long)vecs * VEC; i += TH) term(L::value(base[i]));
         if (csize > 1) cluster_sync();   // the sums have been read
         __syncthreads();
         const int rank = sums.before;
@@ -443,7 +455,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
     }
     if (crank == 0 && warp == 0) {
         // a row that holds a NaN has a NaN in s, one with a +inf gets it here
-        const float s = sums.most == INFINITY ? sums.s - sums.s + NAN : sums.s;
+        const float s = sums.most == INFINITY ? NAN : sums.s;
         const float ln_s = logf(s), log2_s = log2f(s);
         auto logprob = [&](float v) {
             if (v == -INFINITY) return -INFINITY + s * 0.f;
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) k_token_logprobs(LogprobParams 
 // token is replaced by `low`, whose p is 0.
 constexpr int kGradVecs = 4;   // vectors of a thread
 
-template <bool BF16> __global__ void __launch_bounds__(kLpThreads) k_token_logprobs_backward(LogprobGradParams p)
+template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_backward(LogprobGradParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
@@ -511,16 +523,16 @@ template <bool BF16> __global__ void __launch_bounds__(kLpThreads) k_token_logpr
         if (threadIdx.x < head) one(threadIdx.x);
         if (threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
     }
-    for (int v0 = blockIdx.y * kGradVecs * kLpThreads; v0 < vecs; v0 += gridDim.y * kGradVecs * kLpThreads) {
+    for (int v0 = blockIdx.y * kGradVecs * kGradThreads; v0 < vecs; v0 += gridDim.y * kGradVecs * kGradThreads) {
         uint4 in[kGradVecs];
 #pragma unroll
         for (int j = 0; j < kGradVecs; ++j) {
-            const int i = v0 + j * kLpThreads + threadIdx.x;
+            const int i = v0 + j * kGradThreads + threadIdx.x;
             if (i < vecs) in[j] = __ldcs((const uint4 *)(x + head) + i);
         }
 #pragma unroll
         for (int j = 0; j < kGradVecs; ++j) {
-            const int i = v0 + j * kLpThreads + threadIdx.x, id = head + i * VEC;
+            const int i = v0 + j * kGradThreads + threadIdx.x, id = head + i * VEC;
             if (i >= vecs) break;
             float r[VEC];
 #pragma unroll
@@ -559,11 +571,15 @@ template <bool BF16> __global__ void __launch_bounds__(kLpThreads) k_token_logpr
     }
 }
 
-template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &p, int cluster, cudaStream_t s)
+template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, int cluster, cudaStream_t s)
 {
+    if (cluster > 8) {   // beyond the portable size
+        cudaError_t e = cudaFuncSetAttribute((const void *)k_token_logprobs<BF16, TOP, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.rows * cluster);
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(W * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -571,29 +587,39 @@ template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP>, p);
+    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP, W>, p);
+}
+
+template <bool BF16, bool TOP> cudaError_t launch_logprobs_warps(const LogprobParams &p, cudaStream_t s)
+{
+    const long long tile = 32 * kVecs * (BF16 ? 8 : 4), sms = sm_count();   // of a warp
+    int cluster = 1;
+    // few rows: 16 warps a CTA, as many CTAs a row as the SMs allow
+    if (p.rows * 4 <= sms && p.vocab >= 16 * tile) {
+        while (cluster < 16 && p.rows * cluster * 2 <= sms && p.vocab >= 16 * tile * cluster) cluster *= 2;
+        return launch_logprobs<BF16, TOP, 16>(p, cluster, s);
+    }
+    // several rounds of CTAs over the GPU, of at least four tiles each
+    while (cluster < 8 && p.rows * cluster < 6 * sms && p.vocab >= 2 * cluster * 4 * 8 * tile) cluster *= 2;
+    return launch_logprobs<BF16, TOP, 8>(p, cluster, s);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobParams &p, bool bf16, cudaStream_t s)
 {
-    // CTAs of a row: enough for several rounds over the GPU, each with at least a tile
-    const long long tile = (long long)kLpThreads * kVecs * (bf16 ? 8 : 4), slots = 3ll * sm_count();
-    int cluster = 1;
-    while (cluster < kLpCluster && p.rows * cluster < 3 * slots && p.vocab >= 2 * cluster * tile) cluster *= 2;
-    if (bf16) return p.top ? launch_logprobs<true, true>(p, cluster, s) : launch_logprobs<true, false>(p, cluster, s);
-    return p.top ? launch_logprobs<false, true>(p, cluster, s) : launch_logprobs<false, false>(p, cluster, s);
+    if (bf16) return p.top ? launch_logprobs_warps<true, true>(p, s) : launch_logprobs_warps<true, false>(p, s);
+    return p.top ? launch_logprobs_warps<false, true>(p, s) : launch_logprobs_warps<false, false>(p, s);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams &p, bool bf16, cudaStream_t s)
 {
-    const long long each = (long long)kLpThreads * kGradVecs * (bf16 ? 8 : 4);
+    const long long each = (long long)kGradThreads * kGradVecs * (bf16 ? 8 : 4);
     const dim3 grid(p.rows, (unsigned)std::min((p.vocab + each - 1) / each, 65535ll));
     if (bf16)
-        k_token_logprobs_backward<true><<<grid, kLpThreads, 0, s>>>(p);
+        k_token_logprobs_backward<true><<<grid, kGradThreads, 0, s>>>(p);
     else
-        k_token_logprobs_backward<false><<<grid, kLpThreads, 0, s>>>(p);
+        k_token_logprobs_backward<false><<<grid, kGradThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
