@@ -9,12 +9,11 @@
 // whose largest |x c| is 2^22 or more (all logits at the type's lowest value, say) is read
 // again with its maximum m and terms of (x - m) c.
 //
-// The alternatives: a thread's tile of logits is looked at only if the largest of it, which
-// the sums need anyway, is above the n-th best value so far.  What passes goes into a
-// shared buffer of (logit, id) keys; a full buffer is reduced to its largest 32 by sorted
-// lists of 32 a warp.  Where a tile would overfill the buffer (the first one, or logits that
-// rise along the row) the n-th largest of the threads' best keys is a bound that at most n
-// threads pass.
+// The alternatives: the n-th largest of the threads' largest logits is a bound that the n
+// largest logits reach, and few others do.  After the pass only the vectors of the threads
+// that reach it are read once more (some two percent, from L2), a warp for each, and what
+// reaches the bound goes into a buffer of (logit, id) keys; sorted lists of 32 a warp reduce
+// it to its largest 32.  Ties cost more readings, not exactness.
 //
 // What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
 // logits in one for most), so the comparisons for rank and maximum work on packed pairs.
@@ -28,7 +27,6 @@ namespace {
 
 constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
-constexpr int kCand = 2048;       // keys of the buffer
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kFar = 4194304.f; // |x c| from which R would not be exact
 
@@ -135,12 +133,15 @@ template <typename K> __device__ __forceinline__ K warp_merge(K a, K b, int lane
     return v;
 }
 
+// A round looks at 8 warps' vectors of up to 8 logits; the buffer holds twice that.
+constexpr int kRoundWarps = 8, kRoundKeys = kRoundWarps * 32 * 8;
+
 template <int W> struct TopState {
-    u64 cand[kCand];
+    u64 cand[2 * kRoundKeys];
     u64 lists[W][32];
-    u64 best[32];        // the largest so far, falling
-    int have;            // keys in cand
-    float least;         // the value of the n-th best, or -inf
+    u64 best[32];            // the largest so far, falling
+    unsigned short over[W * 32];   // the threads whose largest logit reaches the bound
+    int have, overs;         // keys in cand, threads in over
 };
 
 // The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
@@ -156,7 +157,7 @@ template <int W, typename K> __device__ __forceinline__ K merge_lists(K (*lists)
 }
 
 // Takes the buffer's keys into `best`.  Every thread calls it, with the buffer at rest.
-template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top, int n, int warp, int lane)
+template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top, int warp, int lane)
 {
     const int have = top.have;
     u64 mine = warp == 0 ? top.best[lane] : 0ull;
@@ -165,10 +166,16 @@ template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top,
     mine = merge_lists<W>(top.lists, mine, warp, lane);
     if (warp == 0) {
         top.best[lane] = mine;
-        if (lane == n - 1) top.least = mine ? ord_value((uint32_t)(mine >> 32)) : -INFINITY;
         if (lane == 0) top.have = 0;
     }
     __syncthreads();
+}
+
+// The largest value of the type below v (any but -inf).
+template <bool BF16> __device__ __forceinline__ float value_below(float v)
+{
+    const uint32_t u = __float_as_uint(v), step = BF16 ? 0x10000u : 1u;
+    return __uint_as_float(v == 0.f ? 0x80000000u + step : v > 0.f ? u - step : u + step);
 }
 
 struct Sums {
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
-    constexpr int TH = W * 32, VEC = L::VEC, EACH = VEC * kVecs;   // threads; logits of a vector, of a thread's tile
+    constexpr int TH = W * 32, VEC = L::VEC;   // threads; logits of a vector
     __shared__ Sums s_warp[W], s_cta, s_row;
     __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState<W>) : 16];
     TopState<W> &top = *(TopState<W> *)s_top;
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
     const float mine = has ? L::value(x[given]) : 0.f;
     if (TOP) {
         if (threadIdx.x < 32) top.best[threadIdx.x] = 0;
-        if (threadIdx.x == 0) top.have = 0, top.least = -INFINITY;
+        if (threadIdx.x == 0) top.have = top.overs = 0;
         __syncthreads();
     }
 
@@ -261,7 +268,8 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
         if (TOP && v > -INFINITY) push(top_key(v, id));
     };
     if (crank == 0 && threadIdx.x < head) one(threadIdx.x);
-    if (TOP) __syncthreads();
+    if (crank == csize - 1 && threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
+    const float below = value_below<BF16>(mine);   // v >= mine is v > below
 
     const int tiles = (vecs + kVecs * TH - 1) / (kVecs * TH);
     for (int tile = 0; tile < tiles; ++tile) {
@@ -270,20 +278,18 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
         for (int j = 0; j < kVecs; ++j) v[j] = next[j];
         load(tile + 1, next);
         const int first = id0 + tile * kVecs * TH * VEC;   // the tile's ids
-        const int have = TOP ? top.have : 0;
-        const float least = TOP ? top.least : 0.f;
-
-        float high_of[kVecs], high;   // the thread's largest of each vector, and of the tile
+        float high;   // the thread's largest of the tile
+        if (BF16) {
+            uint32_t m = max_bf16x2(max_bf16x2(v[0].x, v[0].y), max_bf16x2(v[0].z, v[0].w));
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            if (BF16) {
-                const uint32_t m = max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w));
-                high_of[j] = fmaxf(bf_lo(m), bf_hi(m));
-            } else {
-                high_of[j] = fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
-                                   fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w)));
-            }
-            high = j ? fmaxf(high, high_of[j]) : high_of[j];
+            for (int j = 1; j < kVecs; ++j) m = max_bf16x2(m, max_bf16x2(max_bf16x2(v[j].x, v[j].y), max_bf16x2(v[j].z, v[j].w)));
+            high = fmaxf(bf_lo(m), bf_hi(m));
+        } else {
+            high = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) high = fmaxf(high, element<BF16>(v[j], e));
         }
         most = fmaxf(most, high);
         raise(high * c);
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
                         before += (tile * kVecs + j) * TH + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
                     }
             } else if (BF16) {
-                const uint32_t m = bf16_bits(mine) * 0x10001u;
+                const uint32_t m = bf16_bits(given >= last ? below : mine) * 0x10001u;
                 uint32_t count = 0;   // as bf16, at most 16 each
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
@@ -324,79 +330,56 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t is;
-                        if (given >= last)
-                            asm("set.ge.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
-                        else
-                            asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
+                        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
                         asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(is));
                     }
                 }
                 before += (int)bf_lo(count) + (int)bf_hi(count);
-            } else if (given >= last) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) >= mine;
             } else {
+                const float m = given >= last ? below : mine;
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) > mine;
+                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) > m;
             }
-        }
-
-        if (TOP) {
-            // later tiles have higher ids, so that an equal value does not pass
-            const bool pass = high > least;
-            const int passing = __syncthreads_count(pass);
-            if (passing == 0) continue;
-            float bound = least;   // what passes is above `least` and not below `bound`,
-            u64 key_bound = 0;     // its key not below `key_bound`
-            if (have + passing * EACH > kCand) {
-                // the n-th largest of the threads' best values; with ties in it, of their keys
-                const uint32_t mark = pass ? ord_key(high) : 0u;
-                uint32_t(*lists)[32] = (uint32_t(*)[32])top.lists;
-                merge_lists<W>(lists, warp_sort(mark, lane), warp, lane);
-                __syncthreads();
-                const uint32_t nth = lists[0][p.top - 1];
-                bound = ord_value(nth);
-                if (have + __syncthreads_count(mark >= nth) * EACH > kCand) {
-                    u64 key = 0;
-                    if (pass)
-#pragma unroll
-                        for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                            for (int e = 0; e < VEC; ++e)
-                                if (element<BF16>(v[j], e) == high)
-                                    key = max(key, top_key(high, first + (j * TH + threadIdx.x) * VEC + e));
-                    merge_lists<W>(top.lists, warp_sort(key, lane), warp, lane);
-                    __syncthreads();
-                    key_bound = top.lists[0][p.top - 1];
-                }
-            }
-            if (pass && high >= bound)
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-                    if (high_of[j] > least && high_of[j] >= bound)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float u = element<BF16>(v[j], e);
-                            if (u > least && u >= bound) {
-                                const u64 key = top_key(u, first + (j * TH + threadIdx.x) * VEC + e);
-                                if (key >= key_bound) push(key);
-                            }
-                        }
-            // n values at the bound or above it are in the buffer now
-            if (bound > least && threadIdx.x == 0) top.least = bound;
-            __syncthreads();
-            if (top.have > kCand / 2) reduce_buffer(top, p.top, warp, lane);
         }
     }
-    if (TOP) __syncthreads();   // every thread has decided on the buffer of the last tile
-    if (crank == csize - 1 && threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
+
     if (TOP) {
+        const uint32_t mark = most == -INFINITY ? 0u : ord_key(most);
+        uint32_t(*lists)[32] = (uint32_t(*)[32])top.lists;
+        merge_lists<W>(lists, warp_sort(mark, lane), warp, lane);
         __syncthreads();
-        reduce_buffer(top, p.top, warp, lane);
+        const uint32_t bound = max(lists[0][p.top - 1], 1u);
+        if (mark >= bound) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)threadIdx.x;
+        __syncthreads();
+        // each warp takes 32 vectors of one such thread in a round
+        const int each = (tiles * kVecs + 31) / 32, items = top.overs * each;
+        u64 least = 0;   // the n-th best key so far
+        for (int from = 0; from < items; from += kRoundWarps) {
+            const int item = from + warp, i = item % each * 32 + lane;
+            if (warp < kRoundWarps && item < items) {
+                const int at = i * TH + top.over[item / each];
+                if (at < vecs) {
+                    const uint4 v = ld_stream16((const uint4 *)base + at);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float u = element<BF16>(v, e);
+                        if (u > -INFINITY && ord_key(u) >= bound) {
+                            const u64 key = top_key(u, id0 + at * VEC + e);
+                            if (key > least) push(key);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            if (top.have > kRoundKeys) {
+                reduce_buffer(top, warp, lane);
+                least = top.best[p.top - 1];
+            }
+            if (from + kRoundWarps < items) __syncthreads();   // all have decided before the next keys come
+        }
+        reduce_buffer(top, warp, lane);
     }
 
     // join the threads, the warps (by warp 0), the cluster (by every CTA's warp 0)
