@@ -257,6 +257,13 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without an order of memory: no CTA of the cluster ends before all are here.
+__device__ __forceinline__ void cluster_leave()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // A float of another CTA's shared memory: the address of one's own copy, and the rank.
 __device__ __forceinline__ float cluster_load(const float *own, uint32_t rank)
 {

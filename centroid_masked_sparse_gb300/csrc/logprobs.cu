@@ -9,11 +9,12 @@
 // whose largest |x c| is 2^22 or more (all logits at the type's lowest value, say) is read
 // again with its maximum m and terms of (x - m) c.
 //
-// The alternatives: the n-th largest of the threads' largest logits is a bound that the n
-// largest logits reach, and few others do.  After the pass only the vectors of the threads
-// that reach it are read once more (some two percent, from L2), a warp for each, and what
-// reaches the bound goes into a buffer of (logit, id) keys; sorted lists of 32 a warp reduce
-// it to its largest 32.  Ties cost more readings, not exactness.
+// The alternatives: each of the W warps finds the ceil(n / W)-th largest of its threads'
+// largest logits; the lowest of these is a bound that at least n logits reach, and few do.
+// After the pass only the vectors of the threads that reach it are read once more (some two
+// percent, from L2), and what reaches the bound goes into a buffer of (logit, id) keys, which
+// are ranked by counting.  A buffer that does not hold them all (ties by the thousand, rising
+// logits) is filled again in rounds and reduced between them by sorted lists of 32 a warp.
 //
 // What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
 // logits in one for most), so the comparisons for rank and maximum work on packed pairs.
@@ -141,7 +142,8 @@ template <int W> struct TopState {
     u64 lists[W][32];
     u64 best[32];            // the largest so far, falling
     unsigned short over[W * 32];   // the threads whose largest logit reaches the bound
-    int have, overs;         // keys in cand, threads in over
+    uint32_t bounds[W];
+    int have, overs;         // keys in cand (or more, if it is full), threads in over
 };
 
 // The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
@@ -199,7 +201,7 @@ __device__ __forceinline__ Sums warp_join(Sums a)
 }
 
 template <bool BF16, bool TOP, int W>
-__global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams p)
+__global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
@@ -228,9 +230,9 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
             v[j] = i < vecs ? ld_stream16((const uint4 *)base + i) : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
         }
     };
+    const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     uint4 next[kVecs];
     load(0, next);
-    const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     const bool has = given >= 0 && given < p.vocab;
     const float mine = has ? L::value(x[given]) : 0.f;
     if (TOP) {
@@ -258,18 +260,22 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
         s2 = add2(s2, e);
         t2 = fma2(e, d, t2);
     };
-    auto push = [&](u64 key) { top.cand[atomicAdd(&top.have, 1)] = key; };
+    auto push = [&](u64 key) {
+        const int at = atomicAdd(&top.have, 1);
+        if (at < 2 * kRoundKeys) top.cand[at] = key;
+    };
+    auto push_scalar = [&](int id) {
+        const float v = L::value(x[id]);
+        if (v > -INFINITY) push(top_key(v, id));
+    };
     auto one = [&](int id) {   // a scalar before or behind the vectors
         const float v = L::value(x[id]);
         most = fmaxf(most, v);
         raise(v * c);
         add(max_nan(v, low), low);
         before += v > mine || (v == mine && id < given);
-        if (TOP && v > -INFINITY) push(top_key(v, id));
     };
-    if (crank == 0 && threadIdx.x < head) one(threadIdx.x);
-    if (crank == csize - 1 && threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
-    const float below = value_below<BF16>(mine);   // v >= mine is v > below
+    const bool before_it = crank == 0 && threadIdx.x < head, behind_it = crank == csize - 1 && threadIdx.x < p.vocab - tail;
 
     const int tiles = (vecs + kVecs * TH - 1) / (kVecs * TH);
     for (int tile = 0; tile < tiles; ++tile) {
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
                         before += (tile * kVecs + j) * TH + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
                     }
             } else if (BF16) {
-                const uint32_t m = bf16_bits(given >= last ? below : mine) * 0x10001u;
+                const uint32_t m = bf16_bits(given >= last ? value_below<BF16>(mine) : mine) * 0x10001u;   // v >= mine is v > the value below
                 uint32_t count = 0;   // as bf16, at most 16 each
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
                 }
                 before += (int)bf_lo(count) + (int)bf_hi(count);
             } else {
-                const float m = given >= last ? below : mine;
+                const float m = given >= last ? value_below<BF16>(mine) : mine;
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j)
 #pragma unroll
@@ -344,42 +350,87 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
             }
         }
     }
+    if (before_it) one(threadIdx.x);
+    if (behind_it) one(tail + threadIdx.x);
 
     if (TOP) {
         const uint32_t mark = most == -INFINITY ? 0u : ord_key(most);
-        uint32_t(*lists)[32] = (uint32_t(*)[32])top.lists;
-        merge_lists<W>(lists, warp_sort(mark, lane), warp, lane);
+        {
+            uint32_t rest = mark, nth = 0;
+            for (int k = 0; k < (p.top + W - 1) / W; ++k) {
+                nth = __reduce_max_sync(~0u, rest);
+                if (lane == __ffs(__ballot_sync(~0u, rest == nth)) - 1) rest = 0;
+            }
+            if (lane == 0) top.bounds[warp] = nth;
+        }
+        if (before_it) push_scalar(threadIdx.x);
+        if (behind_it) push_scalar(tail + threadIdx.x);
         __syncthreads();
-        const uint32_t bound = max(lists[0][p.top - 1], 1u);
+        uint32_t bound = top.bounds[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) bound = min(bound, top.bounds[w]);
+        bound = max(bound, 1u);
         if (mark >= bound) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)threadIdx.x;
         __syncthreads();
-        // each warp takes 32 vectors of one such thread in a round
-        const int each = (tiles * kVecs + 31) / 32, items = top.overs * each;
-        u64 least = 0;   // the n-th best key so far
-        for (int from = 0; from < items; from += kRoundWarps) {
-            const int item = from + warp, i = item % each * 32 + lane;
-            if (warp < kRoundWarps && item < items) {
-                const int at = i * TH + top.over[item / each];
-                if (at < vecs) {
-                    const uint4 v = ld_stream16((const uint4 *)base + at);
+        auto look = [&](const uint4 &v, int at, u64 least) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float u = element<BF16>(v, e);
-                        if (u > -INFINITY && ord_key(u) >= bound) {
-                            const u64 key = top_key(u, id0 + at * VEC + e);
-                            if (key > least) push(key);
-                        }
-                    }
+            for (int e = 0; e < VEC; ++e) {
+                const float u = element<BF16>(v, e);
+                if (u > -INFINITY && ord_key(u) >= bound) {
+                    const u64 key = top_key(u, id0 + at * VEC + e);
+                    if (key > least) push(key);
                 }
             }
-            __syncthreads();
-            if (top.have > kRoundKeys) {
-                reduce_buffer(top, warp, lane);
-                least = top.best[p.top - 1];
+        };
+        const int each = tiles * kVecs, items = top.overs * each;   // vectors of a thread, of all these
+        for (int i0 = 0; i0 < items; i0 += 4 * TH) {
+            uint4 v[4];
+            int at[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * TH + threadIdx.x;
+                at[k] = i < items ? i % each * TH + top.over[i / each] : vecs;
+                if (at[k] < vecs) v[k] = ld_stream16((const uint4 *)base + at[k]);
             }
-            if (from + kRoundWarps < items) __syncthreads();   // all have decided before the next keys come
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (at[k] < vecs) look(v[k], at[k], 0);
         }
-        reduce_buffer(top, warp, lane);
+        __syncthreads();
+        const int have = top.have;
+        if (have <= TH) {
+            if (threadIdx.x < have) {
+                const u64 key = top.cand[threadIdx.x];
+                int at = 0;
+                for (int k = 0; k < have; ++k) at += top.cand[k] > key;
+                if (at < 32) top.best[at] = key;
+            }
+        } else if (have <= 2 * kRoundKeys) {
+            reduce_buffer(top, warp, lane);
+        } else {
+            // again, in rounds that the buffer holds
+            __syncthreads();
+            if (threadIdx.x == 0) top.have = 0;
+            __syncthreads();
+            if (before_it) push_scalar(threadIdx.x);
+            if (behind_it) push_scalar(tail + threadIdx.x);
+            u64 least = 0;   // the n-th best key so far
+            for (int i0 = 0; i0 < items; i0 += kRoundWarps * 32) {
+                const int i = i0 + threadIdx.x;
+                if (threadIdx.x < kRoundWarps * 32 && i < items) {
+                    const int at = i % each * TH + top.over[i / each];
+                    if (at < vecs) look(ld_stream16((const uint4 *)base + at), at, least);
+                }
+                __syncthreads();
+                if (top.have > kRoundKeys - 16) {   // the scalars come on top of a round
+                    reduce_buffer(top, warp, lane);
+                    least = top.best[p.top - 1];
+                }
+                __syncthreads();   // all have decided before the next keys come
+            }
+            reduce_buffer(top, warp, lane);
+        }
+        __syncthreads();
     }
 
     // join the threads, the warps (by warp 0), the cluster (by every CTA's warp 0)
@@ -460,7 +511,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_token_logprobs(LogprobParams
             if (p.top_logprobs) p.top_logprobs[(long long)row * p.top + lane] = logprob(v);
         }
     }
-    if (csize > 1) cluster_sync();   // the first CTA may still be reading the others' lists
+    if (csize > 1) cluster_leave();   // the first CTA may still be reading the others' lists
 }
 
 // grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))).  The logit of a masked
