@@ -257,11 +257,15 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same without an order of memory: no CTA of the cluster ends before all are here.
-__device__ __forceinline__ void cluster_leave()
+// Its halves without an order of memory: no CTA is past the second before all are past the first.
+__device__ __forceinline__ void cluster_arrive()
 {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    __syncwarp();
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 // A float of another CTA's shared memory: the address of one's own copy, and the rank.

@@ -19,6 +19,7 @@
 // What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
 // logits in one for most), so the comparisons for rank and maximum work on packed pairs.
 #include <algorithm>
+#include <type_traits>
 
 #include "lm_ops.h"
 
@@ -72,6 +73,13 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+__device__ __forceinline__ float is_above(float a, float b)   // 1 or 0
+{
+    float r;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // A word of logits: one fp32 or two bf16.
 template <bool BF16> struct Logits;
 template <> struct Logits<false> {
@@ -108,9 +116,6 @@ template <bool BF16> __device__ __forceinline__ float element(const uint4 &v, in
 
 // What stands in for lower logits: their terms are 0 all the same, and it keeps 0 * -inf out.
 __device__ __forceinline__ float lowest(float factor) { return -1e30f / fmaxf(factor, 1.f); }
-
-// (larger logit, then lower id) as one unsigned key; 0 for a masked token.
-__device__ __forceinline__ u64 top_key(float v, int id) { return v == -INFINITY ? 0ull : argmax_key(v, id); }
 
 // The warp's 32 keys in falling order, and the largest 32 of two such lists.
 template <typename K> __device__ __forceinline__ K exchange(K v, int lane, int step, bool up)
@@ -223,12 +228,19 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     const int v_lo = (int)((long long)all * crank / csize), vecs = (int)((long long)all * (crank + 1) / csize) - v_lo;
     const T *base = x + head + (long long)v_lo * VEC;
     const int id0 = head + v_lo * VEC;
+    const uint4 *at_load = (const uint4 *)base + threadIdx.x;
+    const int tiles = (vecs + kVecs * TH - 1) / (kVecs * TH), whole = vecs / (kVecs * TH);   // the last one may be short
     auto load = [&](int tile, uint4 (&v)[kVecs]) {
+        if (tile < whole) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int i = (tile * kVecs + j) * TH + threadIdx.x;
-            v[j] = i < vecs ? ld_stream16((const uint4 *)base + i) : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
+            for (int j = 0; j < kVecs; ++j) v[j] = ld_stream16(at_load + j * TH);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                v[j] = (tile * kVecs + j) * TH + threadIdx.x < vecs ? ld_stream16(at_load + j * TH)
+                                                                   : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
         }
+        at_load += kVecs * TH;
     };
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     uint4 next[kVecs];
@@ -260,13 +272,26 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         s2 = add2(s2, e);
         t2 = fma2(e, d, t2);
     };
-    auto push = [&](u64 key) {
-        const int at = atomicAdd(&top.have, 1);
-        if (at < 2 * kRoundKeys) top.cand[at] = key;
-    };
-    auto push_scalar = [&](int id) {
-        const float v = L::value(x[id]);
-        if (v > -INFINITY) push(top_key(v, id));
+    u64 count2 = 0;   // logits above `over`, as floats (below 2^24 a thread)
+    auto terms = [&](const uint4 (&v)[kVecs], auto counting, float over) {
+        auto two = [&](float a, float b) {
+            add(a, b);
+            if (decltype(counting)::value) count2 = add2(count2, pair(is_above(a, over), is_above(b, over)));
+        };
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            if (BF16) {
+                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u = max_nan_bf16x2(w[i], low2);
+                    two(bf_lo(u), bf_hi(u));
+                }
+            } else {
+                two(max_nan(__uint_as_float(v[j].x), low), max_nan(__uint_as_float(v[j].y), low));
+                two(max_nan(__uint_as_float(v[j].z), low), max_nan(__uint_as_float(v[j].w), low));
+            }
+        }
     };
     auto one = [&](int id) {   // a scalar before or behind the vectors
         const float v = L::value(x[id]);
@@ -277,7 +302,6 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     };
     const bool before_it = crank == 0 && threadIdx.x < head, behind_it = crank == csize - 1 && threadIdx.x < p.vocab - tail;
 
-    const int tiles = (vecs + kVecs * TH - 1) / (kVecs * TH);
     for (int tile = 0; tile < tiles; ++tile) {
         uint4 v[kVecs];
 #pragma unroll
@@ -299,57 +323,26 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         }
         most = fmaxf(most, high);
         raise(high * c);
+        // Logits that come before the given one: not below it at lower ids, above it at higher
+        // ones; a warp without one that reaches it (near the top: most) does not count.
+        const long long last = first + (long long)kVecs * TH * VEC;
+        const bool count = p.rank && has, here = count && ((first <= given && given < last) || mine <= low);
+        if (count && !here && __any_sync(~0u, high >= mine))
+            terms(v, std::true_type{}, given >= last ? value_below<BF16>(mine) : mine);   // v >= mine is v > the value below
+        else
+            terms(v, std::false_type{}, 0.f);
+        if (here) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            if (BF16) {
-                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            for (int j = 0; j < kVecs; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t u = max_nan_bf16x2(w[i], low2);
-                    add(bf_lo(u), bf_hi(u));
+                for (int e = 0; e < VEC; ++e) {
+                    const int id = first + (j * TH + threadIdx.x) * VEC + e;
+                    const float u = element<BF16>(v[j], e);
+                    before += (tile * kVecs + j) * TH + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
                 }
-            } else {
-                add(max_nan(__uint_as_float(v[j].x), low), max_nan(__uint_as_float(v[j].y), low));
-                add(max_nan(__uint_as_float(v[j].z), low), max_nan(__uint_as_float(v[j].w), low));
-            }
-        }
-
-        if (p.rank && has) {
-            // logits that come before the given one: not below it at lower ids, above it at
-            // higher ones (a masked one would count what stands in for logits behind the last)
-            const long long last = first + (long long)kVecs * TH * VEC;
-            if ((first <= given && given < last) || mine == -INFINITY) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int id = first + (j * TH + threadIdx.x) * VEC + e;
-                        const float u = element<BF16>(v[j], e);
-                        before += (tile * kVecs + j) * TH + threadIdx.x < vecs && (u > mine || (u == mine && id < given));
-                    }
-            } else if (BF16) {
-                const uint32_t m = bf16_bits(given >= last ? value_below<BF16>(mine) : mine) * 0x10001u;   // v >= mine is v > the value below
-                uint32_t count = 0;   // as bf16, at most 16 each
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t is;
-                        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(is) : "r"(w[i]), "r"(m));
-                        asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(is));
-                    }
-                }
-                before += (int)bf_lo(count) + (int)bf_hi(count);
-            } else {
-                const float m = given >= last ? value_below<BF16>(mine) : mine;
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) before += element<BF16>(v[j], e) > m;
-            }
         }
     }
+    before += (int)(unpair(count2).x + unpair(count2).y);
     if (before_it) one(threadIdx.x);
     if (behind_it) one(tail + threadIdx.x);
 
@@ -363,33 +356,46 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             }
             if (lane == 0) top.bounds[warp] = nth;
         }
-        if (before_it) push_scalar(threadIdx.x);
-        if (behind_it) push_scalar(tail + threadIdx.x);
         __syncthreads();
         uint32_t bound = top.bounds[0];
 #pragma unroll
         for (int w = 1; w < W; ++w) bound = min(bound, top.bounds[w]);
-        bound = max(bound, 1u);
-        if (mark >= bound) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)threadIdx.x;
-        __syncthreads();
-        auto look = [&](const uint4 &v, int at, u64 least) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float u = element<BF16>(v, e);
-                if (u > -INFINITY && ord_key(u) >= bound) {
-                    const u64 key = top_key(u, id0 + at * VEC + e);
-                    if (key > least) push(key);
-                }
-            }
+        // what reaches this is above -inf
+        const float reach = bound ? ord_value(bound) : -3.402823466e38f;
+        auto push = [&](float v, int id, u64 least) {
+            const u64 key = argmax_key(v, id);
+            if (key <= least) return;
+            const int at = atomicAdd(&top.have, 1);
+            if (at < 2 * kRoundKeys) top.cand[at] = key;
         };
+        auto look = [&](const uint4 &v, int at, u64 least) {
+            float high;
+            if (BF16) {
+                const uint32_t m = max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w));
+                high = fmaxf(bf_lo(m), bf_hi(m));
+            } else {
+                high = fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+            }
+            if (!(high >= reach)) return;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (element<BF16>(v, e) >= reach) push(element<BF16>(v, e), id0 + at * VEC + e, least);
+        };
+        auto look_at_scalars = [&] {
+            if (before_it && L::value(x[threadIdx.x]) >= reach) push(L::value(x[threadIdx.x]), threadIdx.x, 0);
+            if (behind_it && L::value(x[tail + threadIdx.x]) >= reach) push(L::value(x[tail + threadIdx.x]), tail + threadIdx.x, 0);
+        };
+        if (most >= reach) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)threadIdx.x;
+        look_at_scalars();
+        __syncthreads();
         const int each = tiles * kVecs, items = top.overs * each;   // vectors of a thread, of all these
         for (int i0 = 0; i0 < items; i0 += 4 * TH) {
             uint4 v[4];
             int at[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int i = i0 + k * TH + threadIdx.x;
-                at[k] = i < items ? i % each * TH + top.over[i / each] : vecs;
+                const int i = i0 + k * TH + threadIdx.x, thread = i / each;
+                at[k] = i < items ? (i - thread * each) * TH + top.over[thread] : vecs;
                 if (at[k] < vecs) v[k] = ld_stream16((const uint4 *)base + at[k]);
             }
 #pragma unroll
@@ -402,6 +408,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             if (threadIdx.x < have) {
                 const u64 key = top.cand[threadIdx.x];
                 int at = 0;
+#pragma unroll 8
                 for (int k = 0; k < have; ++k) at += top.cand[k] > key;
                 if (at < 32) top.best[at] = key;
             }
@@ -412,8 +419,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             __syncthreads();
             if (threadIdx.x == 0) top.have = 0;
             __syncthreads();
-            if (before_it) push_scalar(threadIdx.x);
-            if (behind_it) push_scalar(tail + threadIdx.x);
+            look_at_scalars();
             u64 least = 0;   // the n-th best key so far
             for (int i0 = 0; i0 < items; i0 += kRoundWarps * 32) {
                 const int i = i0 + threadIdx.x;
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             if (p.top_logprobs) p.top_logprobs[(long long)row * p.top + lane] = logprob(v);
         }
     }
-    if (csize > 1) cluster_leave();   // the first CTA may still be reading the others' lists
+    if (csize > 1) cluster_arrive(), cluster_wait();   // the first CTA may still be reading the others' lists
 }
 
 // grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))).  The logit of a masked
