@@ -11,10 +11,11 @@
 //
 // The alternatives: each of the W warps finds the ceil(n / W)-th largest of its threads'
 // largest logits; the lowest of these is a bound that at least n logits reach, and few do.
-// After the pass only the vectors of the threads that reach it are read once more (some two
-// percent, from L2), and what reaches the bound goes into a buffer of (logit, id) keys, which
-// are ranked by counting.  A buffer that does not hold them all (ties by the thousand, rising
-// logits) is filled again in rounds and reduced between them by sorted lists of 32 a warp.
+// A thread has kept the largest logit of each of eight groups of its tiles; only groups that
+// reach the bound are read once more (a few hundred vectors, from L2), and what reaches it
+// goes into a buffer of (logit, id) keys, which are ranked by counting.  A buffer that does
+// not hold them all (ties by the thousand, rising logits) is filled again in rounds and
+// reduced between them by sorted lists of 32 a warp.
 //
 // What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
 // logits in one for most), so the comparisons for rank and maximum work on packed pairs.
@@ -27,6 +28,7 @@ namespace mtp {
 
 namespace {
 
+constexpr int W = 8;               // warps of a CTA
 constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
@@ -139,20 +141,22 @@ template <typename K> __device__ __forceinline__ K warp_merge(K a, K b, int lane
     return v;
 }
 
-// A round looks at 8 warps' vectors of up to 8 logits; the buffer holds twice that.
-constexpr int kRoundWarps = 8, kRoundKeys = kRoundWarps * 32 * 8;
+// A round looks at 4 warps' vectors of up to 8 logits; the buffer holds twice that.
+constexpr int kGroups = 8;
+constexpr int kRoundWarps = 4, kRoundKeys = kRoundWarps * 32 * 8;
 
-template <int W> struct TopState {
+struct TopState {
     u64 cand[2 * kRoundKeys];
     u64 lists[W][32];
     u64 best[32];            // the largest so far, falling
-    unsigned short over[W * 32];   // the threads whose largest logit reaches the bound
+    float group[kGroups][W * 32];           // the threads' largest logits by groups of tiles
+    unsigned short over[kGroups * W * 32];  // the groups that reach the bound: group * threads + thread
     uint32_t bounds[W];
-    int have, overs;         // keys in cand (or more, if it is full), threads in over
+    int have, overs;         // keys in cand (or more, if it is full), groups in over
 };
 
 // The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
-template <int W, typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K mine, int warp, int lane)
+template <typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K mine, int warp, int lane)
 {
     lists[warp][lane] = mine;
 #pragma unroll
@@ -164,13 +168,13 @@ template <int W, typename K> __device__ __forceinline__ K merge_lists(K (*lists)
 }
 
 // Takes the buffer's keys into `best`.  Every thread calls it, with the buffer at rest.
-template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top, int warp, int lane)
+__device__ __forceinline__ void reduce_buffer(TopState &top, int warp, int lane)
 {
     const int have = top.have;
     u64 mine = warp == 0 ? top.best[lane] : 0ull;
     for (int at = warp * 32; at < have; at += W * 32)
         mine = warp_merge(mine, warp_sort(at + lane < have ? top.cand[at + lane] : 0ull, lane), lane);
-    mine = merge_lists<W>(top.lists, mine, warp, lane);
+    mine = merge_lists(top.lists, mine, warp, lane);
     if (warp == 0) {
         top.best[lane] = mine;
         if (lane == 0) top.have = 0;
@@ -205,15 +209,15 @@ __device__ __forceinline__ Sums warp_join(Sums a)
     return j;
 }
 
-template <bool BF16, bool TOP, int W>
-__global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams p)
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(W * 32, 4) k_token_logprobs(LogprobParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
     constexpr int TH = W * 32, VEC = L::VEC;   // threads; logits of a vector
     __shared__ Sums s_warp[W], s_cta, s_row;
-    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState<W>) : 16];
-    TopState<W> &top = *(TopState<W> *)s_top;
+    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState) : 16];
+    TopState &top = *(TopState *)s_top;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int csize = (int)cluster_size(), crank = (int)cluster_rank(), row = blockIdx.x / csize;
     const T *x = (const T *)p.logits + row * p.ld;
@@ -302,6 +306,9 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     };
     const bool before_it = crank == 0 && threadIdx.x < head, behind_it = crank == csize - 1 && threadIdx.x < p.vocab - tail;
 
+    const int group_tiles = max(1, (tiles + kGroups - 1) / kGroups);
+    int groups = 0, in_group = 0;
+    float of_group = -INFINITY;
     for (int tile = 0; tile < tiles; ++tile) {
         uint4 v[kVecs];
 #pragma unroll
@@ -323,6 +330,13 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         }
         most = fmaxf(most, high);
         raise(high * c);
+        if (TOP) {
+            of_group = fmaxf(of_group, high);
+            if (++in_group == group_tiles) {
+                top.group[groups++][threadIdx.x] = of_group;
+                of_group = -INFINITY, in_group = 0;
+            }
+        }
         // Logits that come before the given one: not below it at lower ids, above it at higher
         // ones; a warp without one that reaches it (near the top: most) does not count.
         const long long last = first + (long long)kVecs * TH * VEC;
@@ -385,21 +399,29 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             if (before_it && L::value(x[threadIdx.x]) >= reach) push(L::value(x[threadIdx.x]), threadIdx.x, 0);
             if (behind_it && L::value(x[tail + threadIdx.x]) >= reach) push(L::value(x[tail + threadIdx.x]), tail + threadIdx.x, 0);
         };
-        if (most >= reach) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)threadIdx.x;
+        if (in_group) top.group[groups++][threadIdx.x] = of_group;
+        if (most >= reach)
+            for (int k = 0; k < groups; ++k)
+                if (top.group[k][threadIdx.x] >= reach) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)(k * TH + threadIdx.x);
         look_at_scalars();
         __syncthreads();
-        const int each = tiles * kVecs, items = top.overs * each;   // vectors of a thread, of all these
-        for (int i0 = 0; i0 < items; i0 += 4 * TH) {
-            uint4 v[4];
-            int at[4];
+        // vector i of all that the groups in `over` hold
+        const int each = group_tiles * kVecs, items = top.overs * each;
+        auto vector_of = [&](int i) {
+            const int o = i / each, who = top.over[o];
+            return (who / TH * each + i - o * each) * TH + who % TH;
+        };
+        for (int i0 = 0; i0 < items; i0 += 2 * TH) {
+            uint4 v[2];
+            int at[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = i0 + k * TH + threadIdx.x, thread = i / each;
-                at[k] = i < items ? (i - thread * each) * TH + top.over[thread] : vecs;
+            for (int k = 0; k < 2; ++k) {
+                const int i = i0 + k * TH + threadIdx.x;
+                at[k] = i < items ? vector_of(i) : vecs;
                 if (at[k] < vecs) v[k] = ld_stream16((const uint4 *)base + at[k]);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 2; ++k)
                 if (at[k] < vecs) look(v[k], at[k], 0);
         }
         __syncthreads();
@@ -424,7 +446,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             for (int i0 = 0; i0 < items; i0 += kRoundWarps * 32) {
                 const int i = i0 + threadIdx.x;
                 if (threadIdx.x < kRoundWarps * 32 && i < items) {
-                    const int at = i % each * TH + top.over[i / each];
+                    const int at = vector_of(i);
                     if (at < vecs) look(ld_stream16((const uint4 *)base + at), at, least);
                 }
                 __syncthreads();
@@ -611,12 +633,14 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     }
 }
 
-template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, int cluster, cudaStream_t s)
+template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
 {
-    if (cluster > 8) {   // beyond the portable size
-        cudaError_t e = cudaFuncSetAttribute((const void *)k_token_logprobs<BF16, TOP, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least.
+    // 320 rows of 262144 bf16: 49 us with one, 50 with two, 52 with four, 71 with eight; 64
+    // rows in fp32: 22 with eight, 24 with four; one row: 12.5 with eight, 14.5 with sixteen.
+    const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 4ll * sm_count();
+    int cluster = 1;
+    while (cluster < 8 && p.rows * cluster * 2 <= slots && p.vocab >= 2 * cluster * 2 * tile) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.rows * cluster);
     cfg.blockDim = dim3(W * 32);
@@ -627,29 +651,15 @@ template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobP
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP, W>, p);
-}
-
-template <bool BF16, bool TOP> cudaError_t launch_logprobs_warps(const LogprobParams &p, cudaStream_t s)
-{
-    const long long tile = 32 * kVecs * (BF16 ? 8 : 4), sms = sm_count();   // of a warp
-    int cluster = 1;
-    // few rows: 16 warps a CTA, as many CTAs a row as the SMs allow
-    if (p.rows * 4 <= sms && p.vocab >= 16 * tile) {
-        while (cluster < 16 && p.rows * cluster * 2 <= sms && p.vocab >= 16 * tile * cluster) cluster *= 2;
-        return launch_logprobs<BF16, TOP, 16>(p, cluster, s);
-    }
-    // several rounds of CTAs over the GPU, of at least four tiles each
-    while (cluster < 8 && p.rows * cluster < 6 * sms && p.vocab >= 2 * cluster * 4 * 8 * tile) cluster *= 2;
-    return launch_logprobs<BF16, TOP, 8>(p, cluster, s);
+    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobParams &p, bool bf16, cudaStream_t s)
 {
-    if (bf16) return p.top ? launch_logprobs_warps<true, true>(p, s) : launch_logprobs_warps<true, false>(p, s);
-    return p.top ? launch_logprobs_warps<false, true>(p, s) : launch_logprobs_warps<false, false>(p, s);
+    if (bf16) return p.top ? launch_logprobs<true, true>(p, s) : launch_logprobs<true, false>(p, s);
+    return p.top ? launch_logprobs<false, true>(p, s) : launch_logprobs<false, false>(p, s);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams &p, bool bf16, cudaStream_t s)
