@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvAppendParams p)
     const int b = blockIdx.y, h = blockIdx.z >> 1;
     const bool values = blockIdx.z & 1;
     int row0, n;
+    wait_for_previous();
     kv_rows(c, b, &row0, &n);
     const int before = __ldg(c.lengths + b);
     if (n <= 0) return;
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvAppendParams p)
         const float v = finite_bf16(x[i / D * stride + i % D]);
         codes[first * D + i] = kv_code(scale > 0.f ? __fdiv_rn(v, scale) : 0.f, c.format);
     }
+    let_next_start();
 }
 
 }  // namespace
@@ -81,8 +83,7 @@ cudaError_t launch_kv_append(const KvAppendParams &p, cudaStream_t s)
     const int longest = c.starts ? c.max_tokens : c.tokens / c.batch;
     // a run of n tokens reaches at most (n - 1) / P + 2 blocks, (n + P - 2) / P + 1
     const unsigned blocks = (unsigned)(((long long)longest + c.page_tokens - 2) / c.page_tokens + 1);
-    k_kv_append<<<dim3(blocks, c.batch, 2 * c.kv_heads), kAppendThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(k_kv_append, dim3(blocks, c.batch, 2 * c.kv_heads), dim3(kAppendThreads), 0, s, p);
 }
 
 }  // namespace mtp

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
     // the item and its rows; everything that ends the kernel early holds for the whole cluster
     const int split = blockIdx.x, b = blockIdx.z, h = blockIdx.y / p.row_tiles;
     const long long item = (long long)b * gridDim.y + blockIdx.y;
+    wait_for_previous();
     const long long length = __ldg(c.lengths + b);
     int row0, n;
     kv_rows(c, b, &row0, &n);
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
         fetch(it + 3, n_place);
     }
 
+    let_next_start();
     // Join the warps.  Their sums, relative to the CTA's maximum, take the rings' place, columns
     // c of lane group g at word (8c + g) ^ (8 (r / 2 % 4)) of their piece of 128, which keeps a
     // warp's stores off each other's banks.
@@ -566,18 +568,8 @@ template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &
     const size_t smem = kW * 2 * kStage + D / 64 * 2 * NT * 512;
     cudaError_t e = allow_smem((const void *)k_kv_attention<D, INT8, NT>, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.splits, p.c.kv_heads * plan.row_tiles, p.c.batch);
-    cfg.blockDim = dim3(kW * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = plan.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_kv_attention<D, INT8, NT>, p);
+    return launch_clusters(k_kv_attention<D, INT8, NT>, dim3(plan.splits, p.c.kv_heads * plan.row_tiles, p.c.batch), dim3(kW * 32),
+                           plan.cluster, smem, s, p);
 }
 
 template <int D> cudaError_t launch_dim(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)

@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(W * 32, 4) k_token_logprobs(LogprobParams p)
         }
         at_load += kVecs * TH;
     };
+    wait_for_previous();
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     uint4 next[kVecs];
     load(0, next);
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(W * 32, 4) k_token_logprobs(LogprobParams p)
                 }
         }
     }
+    let_next_start();
     before += (int)(unpair(count2).x + unpair(count2).y);
     if (before_it) one(threadIdx.x);
     if (behind_it) one(tail + threadIdx.x);
@@ -552,6 +554,8 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     typedef typename L::type T;
     constexpr int VEC = L::VEC;
     const int row = blockIdx.x;
+    let_next_start();
+    wait_for_previous();
     const T *x = (const T *)p.logits + row * p.ld;
     T *g = (T *)p.grad + row * p.ld_grad;
     const int head = min(p.vocab, (int)((16 - ((uintptr_t)x & 15)) % 16 / sizeof(T)));
@@ -641,17 +645,7 @@ template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &
     const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 4ll * sm_count();
     int cluster = 1;
     while (cluster < 8 && p.rows * cluster * 2 <= slots && p.vocab >= 2 * cluster * 2 * tile) cluster *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows * cluster);
-    cfg.blockDim = dim3(W * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_token_logprobs<BF16, TOP>, p);
+    return launch_clusters(k_token_logprobs<BF16, TOP>, dim3((unsigned)p.rows * cluster), dim3(W * 32), cluster, 0, s, p);
 }
 
 }  // namespace
@@ -667,10 +661,8 @@ cudaError_t launch_token_logprobs_backward(const LogprobGradParams &p, bool bf16
     const long long each = (long long)kGradThreads * kGradVecs * (bf16 ? 8 : 4);
     const dim3 grid(p.rows, (unsigned)std::min((p.vocab + each - 1) / each, 65535ll));
     if (bf16)
-        k_token_logprobs_backward<true><<<grid, kGradThreads, 0, s>>>(p);
-    else
-        k_token_logprobs_backward<false><<<grid, kGradThreads, 0, s>>>(p);
-    return cudaGetLastError();
+        return launch_dependent(k_token_logprobs_backward<true>, grid, dim3(kGradThreads), 0, s, p);
+    return launch_dependent(k_token_logprobs_backward<false>, grid, dim3(kGradThreads), 0, s, p);
 }
 
 }  // namespace mtp

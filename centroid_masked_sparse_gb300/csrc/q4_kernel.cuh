@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         }
         ++l_k;
     };
+    let_next_start();
+    wait_for_previous();
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
         load(i);
@@ -320,8 +322,7 @@ template <int NT, int GROUP, bool ZEROS, int W, int S> cudaError_t launch_q4_war
     cudaError_t e = allow_smem((const void *)k_q4_matvec<NT, GROUP, ZEROS, W, S>, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(std::min(sm_count(), plan.tiles), (p.B + NT * 8 - 1) / (NT * 8));
-    k_q4_matvec<NT, GROUP, ZEROS, W, S><<<grid, W * 32, smem, s>>>(p, plan);
-    return cudaGetLastError();
+    return launch_dependent(k_q4_matvec<NT, GROUP, ZEROS, W, S>, grid, dim3(W * 32), smem, s, p, plan);
 }
 
 // 12 warps where each has more than a round of tiles, else 8, whose CTAs have less to set
