@@ -1,32 +1,48 @@
 // New keys and values into the paged 8-bit cache: one scale per (page, kv head), raised
 // when a new token needs it, in which case the page's earlier codes are rounded again.
+//
+// One CTA per (block that the call reaches, kv head, keys or values): it holds the block's new
+// values in registers between the search for the largest and the rounding, so that they are
+// read once; only blocks of more than 16384 new values are read twice.  Bound by latency for
+// single tokens (64 sequences x 8 heads: 2 x 128 bytes in, 128 out per head and sequence), by
+// HBM and the divisions for prompts.
+#include <algorithm>
+
 #include "lm_ops.h"
 
 namespace mtp {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;   // at most
+constexpr int kAppendVecs = 8;        // vectors of 8 values that a thread holds
 
 // A finite value of a bf16 input: NaN counts as 0, infinities as the largest finite bf16.
-__device__ __forceinline__ float finite_bf16(uint16_t h)
+__device__ __forceinline__ float finite_bf16(float v)
 {
-    const float v = bf16_value(h);
     return v == v ? fminf(fmaxf(v, -3.38953139e38f), 3.38953139e38f) : 0.f;
 }
 
-// One CTA per (block that the call reaches, kv head, keys or values); blockIdx.x counts a
-// sequence's blocks from its first new one.
+struct Eight {
+    float v[8];
+};
+__device__ __forceinline__ Eight finite_values(const uint4 &u)
+{
+    return Eight{finite_bf16(bf_lo(u.x)), finite_bf16(bf_hi(u.x)), finite_bf16(bf_lo(u.y)), finite_bf16(bf_hi(u.y)),
+                 finite_bf16(bf_lo(u.z)), finite_bf16(bf_hi(u.z)), finite_bf16(bf_lo(u.w)), finite_bf16(bf_hi(u.w))};
+}
+
+// blockIdx.x counts a sequence's blocks from its first new one.
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvAppendParams p)
 {
     const KvParams &c = p.c;
     __shared__ float s_max[kAppendThreads / 32];
-    const int b = blockIdx.y, h = blockIdx.z >> 1;
+    const int b = blockIdx.y, h = blockIdx.z >> 1, threads = blockDim.x;
     const bool values = blockIdx.z & 1;
-    int row0, n;
     wait_for_previous();
-    kv_rows(c, b, &row0, &n);
     const int before = __ldg(c.lengths + b);
+    int row0, n;
+    kv_rows(c, b, &row0, &n);
     if (n <= 0) return;
     if (before < 0) {
         if (c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
@@ -34,7 +50,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvAppendParams p)
     }
     // block `at` of the sequence holds its positions [at * P, (at + 1) * P); new tokens are
     // positions [before, before + n)
-    const long long P = c.page_tokens, at = before / P + blockIdx.x;
+    const int P = c.page_tokens;
+    const long long at = before / P + blockIdx.x;
     const long long lo = max((long long)before, at * P), hi = min((long long)before + n, (at + 1) * P);
     if (lo >= hi) return;
     int page = -1;
@@ -43,36 +60,68 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(KvAppendParams p)
         if (c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
         return;
     }
-    const int D = c.dim, first = (int)(lo - at * P), count = (int)(hi - lo);
-    const uint16_t *x = (values ? p.v + h * p.v_head : p.k + h * p.k_head);
+    const int D = c.dim, shift = D == 64 ? 3 : D == 128 ? 4 : 5;   // vectors of a token
+    const int first = (int)(lo - at * P), vecs = (int)(hi - lo) << shift;
+    const uint16_t *x = values ? p.v + h * p.v_head : p.k + h * p.k_head;
     const long long stride = values ? p.v_token : p.k_token;
     x += (row0 + (lo - before)) * stride;
     const long long ph = (long long)page * c.kv_heads + h;
-    uint8_t *codes = (values ? c.v_codes : c.k_codes) + ph * P * D;
+    uint2 *codes = (uint2 *)((values ? c.v_codes : c.k_codes) + ph * P * D);
     float *scale_at = (values ? c.v_scales : c.k_scales) + ph;
+    const float old = first > 0 ? *scale_at : 0.f;
+    auto load = [&](int i) { return ld_ro16(x + (i >> shift) * stride + (i & ((1 << shift) - 1)) * 8); };
 
+    uint4 held[kAppendVecs];
     float top = 0.f;
-    for (int i = threadIdx.x; i < count * D; i += kAppendThreads)
-        top = fmaxf(top, fabsf(finite_bf16(x[i / D * stride + i % D])));
+    auto largest = [&](const uint4 &u) {
+        const Eight e = finite_values(u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(e.v[k]));
+    };
+    const bool holds = vecs <= kAppendVecs * threads;
+    if (holds) {
+#pragma unroll
+        for (int k = 0; k < kAppendVecs; ++k)
+            held[k] = (int)threadIdx.x + k * threads < vecs ? load(threadIdx.x + k * threads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kAppendVecs; ++k) largest(held[k]);
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < vecs; i += threads) largest(load(i));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (threadIdx.x % 32 == 0) s_max[threadIdx.x / 32] = top;
-    const float old = first > 0 ? *scale_at : 0.f;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, s_max[w]);
+    for (int w = 0; w < threads / 32; ++w) top = fmaxf(top, s_max[w]);
     const float scale = fmaxf(old, __fdiv_rn(top, c.format == MTP_KV_INT8 ? 127.f : 448.f));
     if (threadIdx.x == 0) *scale_at = scale;   // every thread has read the old one
     if (scale != old) {
         const float ratio = scale > 0.f ? __fdiv_rn(old, scale) : 0.f;
-        for (int i = threadIdx.x; i < first * D; i += kAppendThreads)
-            codes[i] = kv_code(kv_value(codes[i], c.format) * ratio, c.format);
+        for (int i = threadIdx.x; i < first << shift; i += threads) {
+            uint2 u = codes[i];
+            auto again = [&](uint32_t w) {
+                return kv_codes(kv_value(w, c.format) * ratio, kv_value(w >> 8, c.format) * ratio, kv_value(w >> 16, c.format) * ratio,
+                                kv_value(w >> 24, c.format) * ratio, c.format);
+            };
+            u.x = again(u.x), u.y = again(u.y);
+            codes[i] = u;
+        }
     }
-    for (int i = threadIdx.x; i < count * D; i += kAppendThreads) {
-        const float v = finite_bf16(x[i / D * stride + i % D]);
-        codes[first * D + i] = kv_code(scale > 0.f ? __fdiv_rn(v, scale) : 0.f, c.format);
+    auto store = [&](int i, const uint4 &u) {
+        Eight e = finite_values(u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e.v[k] = scale > 0.f ? __fdiv_rn(e.v[k], scale) : 0.f;
+        codes[(first << shift) + i] = make_uint2(kv_codes(e.v[0], e.v[1], e.v[2], e.v[3], c.format),
+                                                 kv_codes(e.v[4], e.v[5], e.v[6], e.v[7], c.format));
+    };
+    if (holds) {
+#pragma unroll
+        for (int k = 0; k < kAppendVecs; ++k)
+            if ((int)threadIdx.x + k * threads < vecs) store(threadIdx.x + k * threads, held[k]);
+    } else {
+        for (int i = threadIdx.x; i < vecs; i += threads) store(i, load(i));
     }
-    let_next_start();
 }
 
 }  // namespace
@@ -83,7 +132,11 @@ cudaError_t launch_kv_append(const KvAppendParams &p, cudaStream_t s)
     const int longest = c.starts ? c.max_tokens : c.tokens / c.batch;
     // a run of n tokens reaches at most (n - 1) / P + 2 blocks, (n + P - 2) / P + 1
     const unsigned blocks = (unsigned)(((long long)longest + c.page_tokens - 2) / c.page_tokens + 1);
-    return launch_dependent(k_kv_append, dim3(blocks, c.batch, 2 * c.kv_heads), dim3(kAppendThreads), 0, s, p);
+    // a vector a thread for few tokens, four where blocks are long; enough for the earlier codes
+    const int news = std::min(longest, c.page_tokens) * (c.dim / 8), all = c.page_tokens * (c.dim / 8);
+    const int want = std::max(std::min(news, 32), std::max(news / 4, all / 16));
+    const int threads = std::min(kAppendThreads, (want + 31) / 32 * 32);
+    return launch_dependent(k_kv_append, dim3(blocks, c.batch, 2 * c.kv_heads), dim3(threads), 0, s, p);
 }
 
 }  // namespace mtp

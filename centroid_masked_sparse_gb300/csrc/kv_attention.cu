@@ -389,7 +389,6 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
         fetch(it + 3, n_place);
     }
 
-    let_next_start();
     // Join the warps.  Their sums, relative to the CTA's maximum, take the rings' place, columns
     // c of lane group g at word (8c + g) ^ (8 (r / 2 % 4)) of their piece of 128, which keeps a
     // warp's stores off each other's banks.
@@ -515,13 +514,13 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
         else
             *(float4 *)(partial + ck * stride + r * D + word) = v;
     }
+    cluster_arrive();   // this CTA has read the others' sums
     if (clusters == 1) {
         if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
-        cluster_sync();   // the others may still be reading this CTA's sums
+        cluster_wait();   // the others may still be reading this CTA's
         return;
     }
     for (int i = threadIdx.x; i < 3 * R; i += kW * 32) partial[ck * stride + R * D + crank * 3 * R + i] = s_joined[0][i];
-    cluster_sync();
 
     // Join the clusters: the last one to arrive, per slice of columns, in the clusters' order.
     __threadfence();
@@ -533,32 +532,49 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
         __threadfence();
     }
     __syncthreads();
+    cluster_wait();   // the others may still be reading this CTA's sums
     if (!s_last) return;
+    // four words and every fourth cluster at a time, as the threads go; the first sums are on
+    // their way while the weights are found
+    constexpr int LANES = 4, FIRST = 10;
+    const int from = threadIdx.x % LANES, quads = live * width / 4;
+    auto source = [&](int i) { return partial + (i < quads ? i * 4 / width * D + crank * width + i * 4 % width : 0); };
+    float4 first[FIRST];
+    {
+        const float *src = source(threadIdx.x / LANES);
+#pragma unroll
+        for (int k = 0; k < FIRST; ++k)
+            first[k] = from + k * LANES < clusters ? __ldcg((const float4 *)(src + (from + k * LANES) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 8
     for (int i = threadIdx.x; i < clusters * 3 * R; i += kW * 32)
         (&stat[0][0][0])[i] = __ldcg(partial + i / (3 * R) * stride + R * D + crank * 3 * R + i % (3 * R));
     float *weights = sums;   // [cluster][R]
     __syncthreads();
     if (threadIdx.x < R) join(threadIdx.x, clusters, stat, weights, s_joined[0] + threadIdx.x);
     __syncthreads();
-    // four words and every fourth cluster at a time, as the threads go
-    constexpr int LANES = 4;
-    for (int q0 = 0; q0 < live * width / 4; q0 += kW * 32 / LANES) {
-        const int i = q0 + threadIdx.x / LANES, from = threadIdx.x % LANES;
-        const bool in = i < live * width / 4;
-        const int r = in ? i * 4 / width : 0, word = crank * width + (in ? i * 4 % width : 0);
+    for (int q0 = 0; q0 < quads; q0 += kW * 32 / LANES) {
+        const int i = q0 + threadIdx.x / LANES, r = i < quads ? i * 4 / width : 0;
+        const float *src = source(i);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = from; k < clusters; k += LANES) {
-            const float4 x = __ldcg((const float4 *)(partial + k * stride + r * D + word));
+        auto take = [&](int k, const float4 &x) {
             const float f = weights[k * R + r];
             v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        };
+        int k = from;
+        if (q0 == 0) {
+#pragma unroll
+            for (int j = 0; j < FIRST; ++j, k += LANES)
+                if (k < clusters) take(k, first[j]);
         }
+#pragma unroll 8
+        for (; k < clusters; k += LANES) take(k, __ldcg((const float4 *)(src + k * stride)));
 #pragma unroll
         for (int o = 1; o < LANES; o *= 2) {
             v.x += __shfl_xor_sync(~0u, v.x, o), v.y += __shfl_xor_sync(~0u, v.y, o);
             v.z += __shfl_xor_sync(~0u, v.z, o), v.w += __shfl_xor_sync(~0u, v.w, o);
         }
-        if (in && from == 0) finish(r, word, v, s_joined[1][r]);
+        if (i < quads && from == 0) finish(r, crank * width + i * 4 % width, v, s_joined[1][r]);
     }
     if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
 }

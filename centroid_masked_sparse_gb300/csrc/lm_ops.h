@@ -160,23 +160,28 @@ __device__ __forceinline__ void kv_rows(const KvParams &c, int b, int *first, in
 __device__ __forceinline__ float bf16_value(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// Code word -> value and value -> code of the two cache formats.
-__device__ __forceinline__ float kv_value(uint8_t c, int format)
+// A code's value in the two cache formats.
+__device__ __forceinline__ float kv_value(uint32_t c, int format)
 {
     if (format == MTP_KV_INT8) return (float)(int8_t)c;
     uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(c & 255u)));
     float f;
     asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.f32.f16 %0, lo;\n}\n" : "=f"(f) : "r"(h2));
     return f;
 }
 
-__device__ __forceinline__ uint8_t kv_code(float v, int format)
+// Four values -> four codes, the first in the low byte.
+__device__ __forceinline__ uint32_t kv_codes(float a, float b, float c, float d, int format)
 {
-    if (format == MTP_KV_INT8) return (uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(v, -127.f), 127.f));
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
-    return (uint8_t)r;
+    if (format == MTP_KV_INT8) {
+        auto code = [](float v) { return (uint32_t)__float2int_rn(fminf(fmaxf(v, -127.f), 127.f)) & 255u; };
+        return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
+    }
+    uint32_t r;
+    asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+        " mov.b32 %0, {lo, hi};\n}\n" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
 
 // 16 bytes from global to shared memory without a register or L1.
@@ -260,10 +265,10 @@ __device__ __forceinline__ uint32_t fp16_factor_field(uint32_t top) { return top
 __device__ __forceinline__ float fp16_factor_inverse(uint32_t e) { return __uint_as_float(e == 254u ? 0x00400000u : (254u - e) << 23); }
 
 // Every kernel here starts with the first: it may be brought up while the one ahead of it on
-// the stream runs, and touches no memory before that one is through.  The second lets the next
-// kernel be brought up once all CTAs have come to it (an early one fills the SMs that are free
-// first with the next kernel's CTAs: with one CTA per SM that costs nothing, with several it
-// left them uneven: log probabilities of 320 rows 60 instead of 50 us).
+// the stream ends, and touches no memory before that one is through.  The second lets the next
+// kernel be brought up before this one ends; only with one CTA per SM, where the next one's
+// cannot take the places of CTAs to come (with several it left the SMs uneven: attention over
+// 65519 tokens 26 instead of 22 us).
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

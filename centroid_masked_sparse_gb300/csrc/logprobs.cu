@@ -357,7 +357,6 @@ __global__ void __launch_bounds__(W * 32, 4) k_token_logprobs(LogprobParams p)
                 }
         }
     }
-    let_next_start();
     before += (int)(unpair(count2).x + unpair(count2).y);
     if (before_it) one(threadIdx.x);
     if (behind_it) one(tail + threadIdx.x);
@@ -554,7 +553,6 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     typedef typename L::type T;
     constexpr int VEC = L::VEC;
     const int row = blockIdx.x;
-    let_next_start();
     wait_for_previous();
     const T *x = (const T *)p.logits + row * p.ld;
     T *g = (T *)p.grad + row * p.ld_grad;
