@@ -778,7 +778,7 @@ const char *mtp_status_string(mtp_status status)
     return "unknown status";
 }
 
-int32_t mtp_version(void) { return 100; }
+int32_t mtp_version(void) { return 200; }
 
 mtp_status mtp_profile_events(int32_t kernel, void *start_event, void *stop_event)
 {

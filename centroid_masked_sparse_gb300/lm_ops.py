@@ -314,6 +314,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return scored.logprob, scored.entropy
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_logprob, grad_entropy):
         logits, tokens, lse, entropy = ctx.saved_tensors
         grad = mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob.contiguous(),
