@@ -16,7 +16,7 @@
 // row's maximum so far, or up to 8 below it: p stays below 2^8, and most blocks need no
 // maximum across lanes.
 //
-// Split.  A warp reads blocks of 16 tokens, eight kilobytes of codes ahead, each lane the
+// Split.  A warp reads blocks of 16 tokens, two steps ahead, each lane the
 // pieces of its own operands (cp.async into its own slots: no barrier).  The CTAs of an item
 // (a sequence, a kv head, a tile of query rows) share its blocks; eight of them form a
 // cluster and join their sums through distributed shared memory, each one slice of the
@@ -31,7 +31,7 @@ namespace mtp {
 namespace {
 
 constexpr int kW = 4;            // warps of a CTA
-constexpr int kStage = 8192;     // bytes of codes of a step
+template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of codes of a step
 constexpr int kMinBlocks = 16;   // blocks of 16 tokens that a CTA should have at least
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 512;  // the clusters' statistics fit the place of a head of 64
@@ -55,10 +55,21 @@ template <bool INT8> __device__ __forceinline__ void value_operands(uint32_t a, 
     key_operands<INT8>(y, v[2], v[3]);
 }
 
+// Four CTAs per SM (64 ragged sequences, D = 128: 131 us, with three and steps of eight
+// kilobytes 136) where their sums leave the registers for it.
+constexpr int ctas_per_sm(int D, int NT) { return NT > 1 ? 2 : D > 128 ? 3 : 4; }
+// The rings of a CTA's warps, or the sums that take their place.
+constexpr int ring_bytes(int D, int NT)
+{
+    const int ring = kW * 2 * (D == 256 ? kStageOf<256> : kStageOf<64>), sums = kW * NT * 8 * D * 4;
+    return ring > sums ? ring : sums;
+}
+
 // D: columns of a head; NT: query rows / 8.
 template <int D, bool INT8, int NT>
-__global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAttentionParams p)
+__global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(KvAttentionParams p)
 {
+    constexpr int kStage = kStageOf<D>;
     constexpr int U = kStage / (32 * D);       // blocks of 16 tokens in a step
     constexpr int J = D / 64;                  // pieces of 64 columns of a key
     constexpr int MT = D / 16;                 // tiles of 16 columns of a value
@@ -188,7 +199,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
     }
 
     // each row's power of two, and the row in the operand's order
-    uint4 *s_q = (uint4 *)(smem + kW * 2 * kStage);   // [piece of 64][half of a lane's 16][NT][lane]
+    uint4 *s_q = (uint4 *)(smem + ring_bytes(D, NT));   // [piece of 64][half of a lane's 16][NT][lane]
 #pragma unroll
     for (int i = 0; i < QR; ++i) {
         const int r = warp + i * kW;
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) k_kv_attention(KvAtt
 
 template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)
 {
-    const size_t smem = kW * 2 * kStage + D / 64 * 2 * NT * 512;
+    const size_t smem = ring_bytes(D, NT) + D / 64 * 2 * NT * 512;
     cudaError_t e = allow_smem((const void *)k_kv_attention<D, INT8, NT>, smem);
     if (e != cudaSuccess) return e;
     return launch_clusters(k_kv_attention<D, INT8, NT>, dim3(plan.splits, p.c.kv_heads * plan.row_tiles, p.c.batch), dim3(kW * 32),
@@ -608,7 +619,7 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     long long seen = max_len > 0 ? std::min<long long>(max_len, cap) : cap;
     if (window > 0) seen = std::min(seen, window + longest_q - 1);
     // four rounds of CTAs where there are many items, whose lengths may differ
-    const long long slots = (long long)sm_count() * (plan.tiles8 == 1 ? 3 : 2);
+    const long long slots = (long long)sm_count() * ctas_per_sm(c.dim, plan.tiles8);
     const long long most = (seen / 16 + kMinBlocks) / kMinBlocks;
     long long splits = plan.items >= slots / 2 ? 4 * slots / plan.items : slots / plan.items;
     splits = std::max(1ll, std::min({splits, most, (long long)kMaxSplits}));

@@ -119,63 +119,70 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         cp_async_commit();
     }
 
-    // A warp takes batch rows warp, warp + W, ..., eight loads of a lane in flight: first each
-    // row's largest value and its power of two ...
-    for (int n = warp; n < NT * 8; n += W) {
-        uint32_t top = 0;
-        const uint16_t *x = p.x + (b0 + n) * p.ld_x;
-        for (int k = lane * 8; k < p.K && b0 + n < p.B; k += 2048) {
-            uint4 v[8];
+    // A warp takes batch rows warp, warp + W, ..., eight loads of a lane in flight (2048
+    // columns).  x of a chunk is staged in the operand's order: the 16 bytes of lane (g, t) lie
+    // at lane (g ^ (word % 8), t), which spreads a row's words over the banks.  Beside it the
+    // sums of a group's columns, in the place of its first word.
+    auto load_x = [&](uint4 (&u)[8], int n, int k0, int left) {   // columns k0 + lane * 8 + i * 256
+        const uint16_t *x = p.x + (b0 + n) * p.ld_x + k0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k + i * 256 < p.K ? ld_ro16(x + k + i * 256) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) u[i] = i * 256 + lane * 8 < left ? ld_ro16(x + i * 256 + lane * 8) : make_uint4(0, 0, 0, 0);
+    };
+    auto put_x = [&](const uint4 (&u)[8], int n, int w0, int words, float f) {   // words w0 + i * 8 + g
+        uint4 *dst = xs + n / 8 * 32 + ((n % 8 ^ g) * 4 + t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int word = w0 + i * 8 + g;
+            if (w0 + i * 8 >= words) break;   // words is a multiple of 8
+            const float v0 = bf_lo(u[i].x) * f, v1 = bf_hi(u[i].x) * f, v2 = bf_lo(u[i].y) * f, v3 = bf_hi(u[i].y) * f;
+            const float v4 = bf_lo(u[i].z) * f, v5 = bf_hi(u[i].z) * f, v6 = bf_lo(u[i].w) * f, v7 = bf_hi(u[i].w) * f;
+            dst[word * NT * 32] = make_uint4(half_pair(v0, v4), half_pair(v1 * 0.0625f, v5 * 0.0625f), half_pair(v2, v6),
+                                             half_pair(v3 * 0.0625f, v7 * 0.0625f));
+            float sum = ((v0 + v4) + (v1 + v5)) + ((v2 + v6) + (v3 + v7));
+#pragma unroll
+            for (int o = 1; o < 4 * WORDS; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+            if (lane % (4 * WORDS) == 0) xw[word * NT * 8 + n] = sum * ((ZEROS ? -1.f : -8.f) / 16777216.f);
+        }
+    };
+    auto words_of = [&](int c) { return min(plan.chunk, all_steps * kCols - c * plan.chunk) / 32; };
+    auto stage_x = [&](int c, int n, int w0) {   // the row's words of a chunk from w0 on
+        for (; w0 < words_of(c); w0 += 64) {
+            uint4 u[8];
+            load_x(u, n, c * plan.chunk + w0 * 32, b0 + n < p.B ? p.K - c * plan.chunk - w0 * 32 : 0);
+            put_x(u, n, w0, words_of(c), s_factor[n]);
+        }
+    };
+    // each row's largest value and its power of two, and the first chunk
+    for (int n = warp; n < NT * 8; n += W) {
+        const int left = b0 + n < p.B ? p.K : 0;
+        uint4 u[8];
+        load_x(u, n, 0, left);
+        uint32_t top = 0;
+        auto largest = [&](const uint4 (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
                                              __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        };
+        largest(u);
+        for (int k = 2048; k < left; k += 2048) {
+            uint4 v[8];
+            load_x(v, n, k, left - k);
+            largest(v);
         }
-        top = max(top >> 16, top & 0xffffu);
-        top = __reduce_max_sync(~0u, top);
+        top = __reduce_max_sync(~0u, max(top >> 16, top & 0xffffu));
+        const uint32_t e = fp16_factor_field(top);
+        const float f = __uint_as_float(e << 23);
         if (lane == 0) {
-            const uint32_t e = fp16_factor_field(top);
-            s_factor[n] = __uint_as_float(e << 23);
+            s_factor[n] = f;
             // a row that holds a NaN or an infinity gives NaN
             s_inverse[n] = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fp16_factor_inverse(e);
         }
+        __syncwarp();
+        put_x(u, n, 0, words_of(0), f);
+        stage_x(0, n, 64);
     }
-    __syncwarp();
-    // ... then x of a chunk in the operand's order: the 16 bytes of lane (g, t) lie at lane
-    // (g ^ (word % 8), t), which spreads a row's words over the banks.  Beside it the sums of
-    // a group's columns, in the place of its first word.
-    auto stage_x = [&](int c) {
-        const int k0 = c * plan.chunk, words = min(plan.chunk, all_steps * kCols - k0) / 32;
-        for (int n = warp; n < NT * 8; n += W) {
-            const uint16_t *x = p.x + (b0 + n) * p.ld_x + k0;
-            const int left = b0 + n < p.B ? p.K - k0 : 0;
-            const float f = s_factor[n];
-            uint4 *dst = xs + n / 8 * 32 + ((n % 8 ^ g) * 4 + t);   // of word i * 8 + g
-            for (int w0 = 0; w0 < words; w0 += 64) {
-                uint4 u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int k = (w0 + i * 8) * 32 + lane * 8;
-                    u[i] = k < left ? ld_ro16(x + k) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int word = w0 + i * 8 + g;
-                    if (w0 + i * 8 >= words) break;   // words is a multiple of 8
-                    const float v0 = bf_lo(u[i].x) * f, v1 = bf_hi(u[i].x) * f, v2 = bf_lo(u[i].y) * f, v3 = bf_hi(u[i].y) * f;
-                    const float v4 = bf_lo(u[i].z) * f, v5 = bf_hi(u[i].z) * f, v6 = bf_lo(u[i].w) * f, v7 = bf_hi(u[i].w) * f;
-                    dst[word * NT * 32] = make_uint4(half_pair(v0, v4), half_pair(v1 * 0.0625f, v5 * 0.0625f), half_pair(v2, v6),
-                                                     half_pair(v3 * 0.0625f, v7 * 0.0625f));
-                    float sum = ((v0 + v4) + (v1 + v5)) + ((v2 + v6) + (v3 + v7));
-#pragma unroll
-                    for (int o = 1; o < 4 * WORDS; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
-                    if (lane % (4 * WORDS) == 0) xw[word * NT * 8 + n] = sum * ((ZEROS ? -1.f : -8.f) / 16777216.f);
-                }
-            }
-        }
-    };
+    __syncthreads();
 
     float acc[kTiles][NT][4];
 #pragma unroll
@@ -197,9 +204,9 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     for (int round = 0; round < rounds; ++round) {
         const int tile = t_lo + round * kTiles, live = min(t_hi - tile, kTiles);
         for (int c = 0; c < chunks; ++c) {
-            if (chunks > 1 || round == 0) {
-                if (chunks > 1) __syncthreads();
-                stage_x(c);
+            if (round + c > 0 && chunks > 1) {
+                __syncthreads();
+                for (int n = warp; n < NT * 8; n += W) stage_x(c, n, 0);
                 __syncthreads();
             }
             int k, k_hi;
