@@ -28,7 +28,6 @@ namespace mtp {
 
 namespace {
 
-constexpr int W = 8;               // warps of a CTA
 constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
@@ -145,7 +144,7 @@ template <typename K> __device__ __forceinline__ K warp_merge(K a, K b, int lane
 constexpr int kGroups = 8;
 constexpr int kRoundWarps = 4, kRoundKeys = kRoundWarps * 32 * 8;
 
-struct TopState {
+template <int W> struct TopState {
     u64 cand[2 * kRoundKeys];
     u64 lists[W][32];
     u64 best[32];            // the largest so far, falling
@@ -156,7 +155,7 @@ struct TopState {
 };
 
 // The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
-template <typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K mine, int warp, int lane)
+template <int W, typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K mine, int warp, int lane)
 {
     lists[warp][lane] = mine;
 #pragma unroll
@@ -168,13 +167,13 @@ template <typename K> __device__ __forceinline__ K merge_lists(K (*lists)[32], K
 }
 
 // Takes the buffer's keys into `best`.  Every thread calls it, with the buffer at rest.
-__device__ __forceinline__ void reduce_buffer(TopState &top, int warp, int lane)
+template <int W> __device__ __forceinline__ void reduce_buffer(TopState<W> &top, int warp, int lane)
 {
     const int have = top.have;
     u64 mine = warp == 0 ? top.best[lane] : 0ull;
     for (int at = warp * 32; at < have; at += W * 32)
         mine = warp_merge(mine, warp_sort(at + lane < have ? top.cand[at + lane] : 0ull, lane), lane);
-    mine = merge_lists(top.lists, mine, warp, lane);
+    mine = merge_lists<W>(top.lists, mine, warp, lane);
     if (warp == 0) {
         top.best[lane] = mine;
         if (lane == 0) top.have = 0;
@@ -209,15 +208,15 @@ __device__ __forceinline__ Sums warp_join(Sums a)
     return j;
 }
 
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(W * 32, 4) k_token_logprobs(LogprobParams p)
+template <bool BF16, bool TOP, int W>
+__global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
     constexpr int TH = W * 32, VEC = L::VEC;   // threads; logits of a vector
     __shared__ Sums s_warp[W], s_cta, s_row;
-    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState) : 16];
-    TopState &top = *(TopState *)s_top;
+    __shared__ __align__(16) unsigned char s_top[TOP ? sizeof(TopState<W>) : 16];
+    TopState<W> &top = *(TopState<W> *)s_top;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int csize = (int)cluster_size(), crank = (int)cluster_rank(), row = blockIdx.x / csize;
     const T *x = (const T *)p.logits + row * p.ld;
@@ -635,23 +634,31 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     }
 }
 
-template <bool BF16, bool TOP> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
+template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
 {
-    // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least.
-    // 320 rows of 262144 bf16: 49 us with one, 50 with two, 52 with four, 71 with eight; 64
-    // rows in fp32: 22 with eight, 24 with four; one row: 12.5 with eight, 14.5 with sixteen.
-    const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 4ll * sm_count();
+    // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least
+    // (64 rows in fp32: 22 us with eight, 24 with four; one row: 12.5 with eight, 14.5 with
+    // sixteen)
+    const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 32ll / W * sm_count();
     int cluster = 1;
     while (cluster < 8 && p.rows * cluster * 2 <= slots && p.vocab >= 2 * cluster * 2 * tile) cluster *= 2;
-    return launch_clusters(k_token_logprobs<BF16, TOP>, dim3((unsigned)p.rows * cluster), dim3(W * 32), cluster, 0, s, p);
+    return launch_clusters(k_token_logprobs<BF16, TOP, W>, dim3((unsigned)p.rows * cluster), dim3(W * 32), cluster, 0, s, p);
+}
+
+// Many rows: CTAs of four warps, whose searches for alternatives hold up less (2000 rows of
+// 32003 bf16: 39 us, with eight warps 47; 320 of 262144: 46 and 47).  Few: eight (64 rows of
+// 262144 fp32: 20 us, with four warps 22.5; one row: 10.6 and 12.6).
+template <bool BF16, bool TOP> cudaError_t launch_logprobs_rows(const LogprobParams &p, cudaStream_t s)
+{
+    return p.rows > 2 * sm_count() ? launch_logprobs<BF16, TOP, 4>(p, s) : launch_logprobs<BF16, TOP, 8>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobParams &p, bool bf16, cudaStream_t s)
 {
-    if (bf16) return p.top ? launch_logprobs<true, true>(p, s) : launch_logprobs<true, false>(p, s);
-    return p.top ? launch_logprobs<false, true>(p, s) : launch_logprobs<false, false>(p, s);
+    if (bf16) return p.top ? launch_logprobs_rows<true, true>(p, s) : launch_logprobs_rows<true, false>(p, s);
+    return p.top ? launch_logprobs_rows<false, true>(p, s) : launch_logprobs_rows<false, false>(p, s);
 }
 
 cudaError_t launch_token_logprobs_backward(const LogprobGradParams &p, bool bf16, cudaStream_t s)
