@@ -12,6 +12,8 @@ get_top_tokens, ``mtp_masked_scatter_logits`` is forward,
 ``mtp_centroid_scores`` is the centroid Linear + topk of _select_and_score,
 and ``mtp_dense_lm_head`` is the dense comparator (compute_logits without the
 masked embedder, no softcapping).
+
+The operators around the head (include/mtp_lm_ops.h) are in ``lm_ops`` and reached from here.
 """
 from __future__ import annotations
 

@@ -22,6 +22,13 @@
 // cluster and join their sums through distributed shared memory, each one slice of the
 // head's columns.  Only an item with more than one cluster goes through global memory: the
 // last cluster to arrive, per slice, adds the others' sums in their order.
+//
+// What bounds it: latency.  64 ragged sequences of up to 8191 tokens (8 kv heads of 128, 617
+// MB) take 131 us, 4.7 TB/s, with instructions in 0.36 of the issue slots and the tensor pipe
+// 13 % busy.  One sequence of 65519 tokens (one kv head of 256, 33.6 MB) takes 21.5 us: its
+// chain of look-ups, few steps and joins.  16 sequences of up to five query tokens in a window
+// of 512 take 14.4 us, 8 of them the host's call.  A warp per query row on the CUDA cores took
+// 20.8 ms, 3 ms and 138 us.
 #include <algorithm>
 
 #include "lm_ops.h"
@@ -32,7 +39,10 @@ namespace {
 
 constexpr int kW = 4;            // warps of a CTA
 template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of codes of a step
-constexpr int kMinBlocks = 16;   // blocks of 16 tokens that a CTA should have at least
+// Blocks of 16 tokens that a CTA should have at least.  A grid fills the GPU once or a little
+// more: the ragged sequences with 1, 2, 4, 8 CTAs an item 147, 141, 139, 171 us, the long one
+// with 152, 256, 304, 456 CTAs in all 26.5, 21.9, 25.7, 36 us.
+constexpr int kMinBlocks = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 512;  // the clusters' statistics fit the place of a head of 64
 

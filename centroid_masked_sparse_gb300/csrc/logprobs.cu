@@ -17,8 +17,9 @@
 // not hold them all (ties by the thousand, rising logits) is filled again in rounds and
 // reduced between them by sorted lists of 32 a warp.
 //
-// What bounds it: HBM for fp32; for bf16 the instruction issue comes close (six a logit, two
-// logits in one for most), so the comparisons for rank and maximum work on packed pairs.
+// What bounds it: HBM for fp32; for bf16 instructions, 13 for two logits, although sums and
+// comparisons work on packed pairs: 320 rows of 262144 take 45.6 us with 8 alternatives, 3.7
+// TB/s.  One row takes 10.6 us: the host's call is 7, the rest the cluster's joins.
 #include <algorithm>
 #include <type_traits>
 
@@ -543,7 +544,8 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
 }
 
 // grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))).  The logit of a masked
-// token is replaced by `low`, whose p is 0.
+// token is replaced by `low`, whose p is 0.  Bound by HBM: 1024 rows of 262144 bf16 take 159
+// us, 99 % of a copy's rate; 61 rows of 32003 6.6 us, the time of the host's call.
 constexpr int kGradVecs = 4;   // vectors of a thread
 
 template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_backward(LogprobGradParams p)
@@ -637,8 +639,8 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
 template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
 {
     // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least
-    // (64 rows in fp32: 22 us with eight, 24 with four; one row: 12.5 with eight, 14.5 with
-    // sixteen)
+    // (launches one after the other; 64 rows in fp32: 22 us with eight, 24 with four; one
+    // row: 12.5 with eight, 14.5 with sixteen)
     const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 32ll / W * sm_count();
     int cluster = 1;
     while (cluster < 8 && p.rows * cluster * 2 <= slots && p.vocab >= 2 * cluster * 2 * tile) cluster *= 2;

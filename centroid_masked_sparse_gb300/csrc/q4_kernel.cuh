@@ -17,10 +17,11 @@
 // Both, times the group's scale, are added to the row's sum in fp32.
 //
 // What bounds it.  HBM up to 8 batch rows: 4.25 bits a weight with groups of 64; 262144 x
-// 1536 with 8 rows takes 43 us, 5.1 TB/s, the same loads and stores without the products
-// 41.7.  Above, the products: the tensor pipe takes 8 cycles for each mma and is 46 % busy
-// at 16 rows (56 us), 88 us at 32.  Unpacking to bf16 with a subtraction of the zero point
-// took 23 integer instructions for every 8 here (and that kernel 61 us at 8 rows).
+// 1536 with 8 rows takes 39.8 us behind another launch, 5.6 TB/s, the same loads and stores
+// without the products about 2 us less.  Above, the products and what feeds them: 51.5 us at
+// 16 rows, 82.6 at 32; 50021 x 2592 with 23 rows takes 38 us with the tensor pipe 35 % busy,
+// one round of tiles a warp and x in two chunks.  Unpacking to bf16 with a subtraction of the
+// zero point took 23 integer instructions for every 8 here (61 us at 8 rows).
 #pragma once
 
 #include <algorithm>
@@ -333,7 +334,7 @@ template <int NT, int GROUP, bool ZEROS, int W, int S> cudaError_t launch_q4_war
 }
 
 // 12 warps where each has more than a round of tiles, else 8, whose CTAs have less to set
-// up (262144 x 1536, 8 rows: 12 warps 43.3, 16 warps 45.5 us; 50021 x 2592, 23 rows: 43
+// up (launches one after the other; 262144 x 1536, 8 rows: 12 warps 43.3, 16 warps 45.5 us; 50021 x 2592, 23 rows: 43
 // with 12, 55 with 8, 53 with 16; 30000 x 2048, 8 rows: 14.6 with 12, 12.5 with 8, 16.7
 // with 16).  Three slots if x fits beside them (262144 x 1536, 8 rows: 45.3 with two).  With
 // x in chunks 8 warps are ahead up to 8 batch rows (65536 x 8192: 70 against 93 us), 12
