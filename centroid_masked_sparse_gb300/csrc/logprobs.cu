@@ -11,15 +11,16 @@
 //
 // The alternatives: each of the W warps finds the ceil(n / W)-th largest of its threads'
 // largest logits; the lowest of these is a bound that at least n logits reach, and few do.
-// A thread has kept the largest logit of each of eight groups of its tiles; only groups that
-// reach the bound are read once more (a few hundred vectors, from L2), and what reaches it
-// goes into a buffer of (logit, id) keys, which are ranked by counting.  A buffer that does
-// not hold them all (ties by the thousand, rising logits) is filled again in rounds and
-// reduced between them by sorted lists of 32 a warp.
+// A thread has kept the largest logit of each of 32 groups of its tiles; only groups that
+// reach the bound are read once more (a few hundred vectors), and what reaches it goes into a
+// buffer of (logit, id) keys, which are ranked by counting.  Where the buffer does not hold
+// them all (ties by the thousand), all vectors are read again in rounds that it holds, with
+// sorted lists of 32 a warp between them.
 //
 // What bounds it: HBM for fp32; for bf16 instructions, 13 for two logits, although sums and
-// comparisons work on packed pairs: 320 rows of 262144 take 45.6 us with 8 alternatives, 3.7
-// TB/s.  One row takes 10.6 us: the host's call is 7, the rest the cluster's joins.
+// comparisons work on packed pairs: 320 rows of 262144 take 42.4 us with 20 alternatives, 4.0
+// TB/s, and 33.8 with none; in fp32 60 us, 5.6 TB/s.  One row takes 9.4 us: the host's call is
+// 7, the rest the cluster's joins.
 #include <algorithm>
 #include <type_traits>
 
@@ -141,18 +142,22 @@ template <typename K> __device__ __forceinline__ K warp_merge(K a, K b, int lane
     return v;
 }
 
-// A round looks at 4 warps' vectors of up to 8 logits; the buffer holds twice that.
-constexpr int kGroups = 8;
-constexpr int kRoundWarps = 4, kRoundKeys = kRoundWarps * 32 * 8;
+// Shared memory is what the loads in flight leave of L1, so the keys take the groups' place.
+constexpr int kGroups = 32, kOvers = 64;
 
 template <int W> struct TopState {
-    u64 cand[2 * kRoundKeys];
+    static constexpr int kKeys = W * 32 * 8;   // what one vector of every thread may bring
+    union {
+        // the threads' largest logits by groups of tiles: bf16, rounded up; the padding spreads
+        // a thread's groups over the banks
+        unsigned short group[kGroups][W * 32 + 2];
+        u64 cand[kKeys];
+    };
     u64 lists[W][32];
-    u64 best[32];            // the largest so far, falling
-    float group[kGroups][W * 32];           // the threads' largest logits by groups of tiles
-    unsigned short over[kGroups * W * 32];  // the groups that reach the bound: group * threads + thread
+    u64 best[32];                      // the largest so far, falling
+    unsigned short over[W][kOvers];    // a warp's groups that reach the bound: group * threads + thread
     uint32_t bounds[W];
-    int have, overs;         // keys in cand (or more, if it is full), groups in over
+    int have, many;                    // keys in cand (or more, if it is full); whether an `over` was too short
 };
 
 // The largest 32 of all warps' lists, falling: warp 0's result, and after a barrier lists[0].
@@ -187,6 +192,13 @@ template <bool BF16> __device__ __forceinline__ float value_below(float v)
 {
     const uint32_t u = __float_as_uint(v), step = BF16 ? 0x10000u : 1u;
     return __uint_as_float(v == 0.f ? 0x80000000u + step : v > 0.f ? u - step : u + step);
+}
+
+// The smallest bf16 from v up; for a NaN any value.
+__device__ __forceinline__ unsigned short bf16_up(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return (unsigned short)((u + (u >> 31 ? 0u : 0xffffu)) >> 16);
 }
 
 struct Sums {
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     const float mine = has ? L::value(x[given]) : 0.f;
     if (TOP) {
         if (threadIdx.x < 32) top.best[threadIdx.x] = 0;
-        if (threadIdx.x == 0) top.have = top.overs = 0;
+        if (threadIdx.x == 0) top.have = top.many = 0;
         __syncthreads();
     }
 
@@ -298,8 +310,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             }
         }
     };
-    auto one = [&](int id) {   // a scalar before or behind the vectors
-        const float v = L::value(x[id]);
+    auto one = [&](int id, float v) {   // a scalar before or behind the vectors
         most = fmaxf(most, v);
         raise(v * c);
         add(max_nan(v, low), low);
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         if (TOP) {
             of_group = fmaxf(of_group, high);
             if (++in_group == group_tiles) {
-                top.group[groups++][threadIdx.x] = of_group;
+                top.group[groups++][threadIdx.x] = bf16_up(of_group);
                 of_group = -INFINITY, in_group = 0;
             }
         }
@@ -358,8 +369,9 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         }
     }
     before += (int)(unpair(count2).x + unpair(count2).y);
-    if (before_it) one(threadIdx.x);
-    if (behind_it) one(tail + threadIdx.x);
+    const float v_before = before_it ? L::value(x[threadIdx.x]) : 0.f, v_behind = behind_it ? L::value(x[tail + threadIdx.x]) : 0.f;
+    if (before_it) one(threadIdx.x, v_before);
+    if (behind_it) one(tail + threadIdx.x, v_behind);
 
     if (TOP) {
         const uint32_t mark = most == -INFINITY ? 0u : ord_key(most);
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             const u64 key = argmax_key(v, id);
             if (key <= least) return;
             const int at = atomicAdd(&top.have, 1);
-            if (at < 2 * kRoundKeys) top.cand[at] = key;
+            if (at < TopState<W>::kKeys) top.cand[at] = key;
         };
         auto look = [&](const uint4 &v, int at, u64 least) {
             float high;
@@ -397,37 +409,51 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
                 if (element<BF16>(v, e) >= reach) push(element<BF16>(v, e), id0 + at * VEC + e, least);
         };
         auto look_at_scalars = [&] {
-            if (before_it && L::value(x[threadIdx.x]) >= reach) push(L::value(x[threadIdx.x]), threadIdx.x, 0);
-            if (behind_it && L::value(x[tail + threadIdx.x]) >= reach) push(L::value(x[tail + threadIdx.x]), tail + threadIdx.x, 0);
+            if (before_it && v_before >= reach) push(v_before, threadIdx.x, 0);
+            if (behind_it && v_behind >= reach) push(v_behind, tail + threadIdx.x, 0);
         };
-        if (in_group) top.group[groups++][threadIdx.x] = of_group;
-        if (most >= reach)
-            for (int k = 0; k < groups; ++k)
-                if (top.group[k][threadIdx.x] >= reach) top.over[atomicAdd(&top.overs, 1)] = (unsigned short)(k * TH + threadIdx.x);
-        look_at_scalars();
-        __syncthreads();
-        // vector i of all that the groups in `over` hold
-        const int each = group_tiles * kVecs, items = top.overs * each;
-        auto vector_of = [&](int i) {
-            const int o = i / each, who = top.over[o];
-            return (who / TH * each + i - o * each) * TH + who % TH;
-        };
-        for (int i0 = 0; i0 < items; i0 += 2 * TH) {
-            uint4 v[2];
-            int at[2];
+        if (in_group) top.group[groups++][threadIdx.x] = bf16_up(of_group);
+        // The groups that reach it: the warp looks at one thread's after the other, a lane each.
+        __syncwarp();
+        const int each = group_tiles * kVecs;   // vectors of a group
+        int overs = 0;
+        for (uint32_t left = __ballot_sync(~0u, most >= reach); left; left &= left - 1) {
+            const int who = warp * 32 + __ffs(left) - 1;
+            const bool reaches = lane < groups && bf_lo(top.group[lane][who]) >= reach;
+            const uint32_t all_reach = __ballot_sync(~0u, reaches);
+            const int at = overs + __popc(all_reach & ((1u << lane) - 1));
+            if (reaches && at < kOvers) top.over[warp][at] = (unsigned short)(lane * TH + who);
+            overs += __popc(all_reach);
+        }
+        if (overs > kOvers) top.many = 1, overs = 0;
+        __syncwarp();
+        const int items = overs * each;
+        uint4 v[2];
+        int at[2];
+        auto load_items = [&](int i0) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int i = i0 + k * TH + threadIdx.x;
-                at[k] = i < items ? vector_of(i) : vecs;
+                const int i = i0 + k * 32 + lane;
+                at[k] = vecs;
+                if (i < items) {
+                    const int o = i / each, who = top.over[warp][o];
+                    at[k] = (who / TH * each + i - o * each) * TH + who % TH;
+                }
                 if (at[k] < vecs) v[k] = ld_stream16((const uint4 *)base + at[k]);
             }
+        };
+        load_items(0);
+        __syncthreads();   // the groups have been read
+        look_at_scalars();
+        for (int i0 = 0; i0 < items; i0 += 64) {
+            if (i0) load_items(i0);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
                 if (at[k] < vecs) look(v[k], at[k], 0);
         }
         __syncthreads();
         const int have = top.have;
-        if (have <= TH) {
+        if (have <= TH && !top.many) {
             if (threadIdx.x < have) {
                 const u64 key = top.cand[threadIdx.x];
                 int at = 0;
@@ -435,35 +461,33 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
                 for (int k = 0; k < have; ++k) at += top.cand[k] > key;
                 if (at < 32) top.best[at] = key;
             }
-        } else if (have <= 2 * kRoundKeys) {
+        } else if (have <= TopState<W>::kKeys && !top.many) {
             reduce_buffer(top, warp, lane);
         } else {
-            // again, in rounds that the buffer holds
+            // all vectors, in rounds that the buffer holds
             __syncthreads();
             if (threadIdx.x == 0) top.have = 0;
             __syncthreads();
             look_at_scalars();
-            u64 least = 0;   // the n-th best key so far
-            for (int i0 = 0; i0 < items; i0 += kRoundWarps * 32) {
+            __syncthreads();
+            reduce_buffer(top, warp, lane);
+            u64 least = top.best[p.top - 1];   // the n-th best key so far
+            for (int i0 = 0; i0 < vecs; i0 += TH) {
                 const int i = i0 + threadIdx.x;
-                if (threadIdx.x < kRoundWarps * 32 && i < items) {
-                    const int at = vector_of(i);
-                    if (at < vecs) look(ld_stream16((const uint4 *)base + at), at, least);
-                }
+                if (i < vecs) look(ld_stream16((const uint4 *)base + i), i, least);
                 __syncthreads();
-                if (top.have > kRoundKeys - 16) {   // the scalars come on top of a round
+                if (top.have > 0) {
                     reduce_buffer(top, warp, lane);
                     least = top.best[p.top - 1];
                 }
                 __syncthreads();   // all have decided before the next keys come
             }
-            reduce_buffer(top, warp, lane);
         }
         __syncthreads();
     }
 
     // join the threads, the warps (by warp 0), the cluster (by every CTA's warp 0)
-    auto join_all = [&](Sums a) {
+    auto join_all = [&](Sums a, bool lists) {
         a = warp_join(a);
         if (lane == 0) s_warp[warp] = a;
         __syncthreads();
@@ -482,13 +506,24 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
                 }
                 b = warp_join(b);
                 if (lane == 0) s_row = b;
+            } else if (TOP && lists && crank == 0 && warp == 1) {
+                // meanwhile the CTAs' alternatives
+                const float *other = (const float *)&top.best[lane];
+                u64 best = top.best[lane];
+                float low_half = cluster_load(other, 1), high_half = cluster_load(other + 1, 1);
+                for (int k = 1; k < csize; ++k) {
+                    const u64 key = (u64)__float_as_uint(low_half) | (u64)__float_as_uint(high_half) << 32;
+                    if (k + 1 < csize) low_half = cluster_load(other, k + 1), high_half = cluster_load(other + 1, k + 1);
+                    best = warp_merge(best, key, lane);
+                }
+                top.best[lane] = best;
             }
         }
         __syncthreads();
         return s_row;
     };
     const float2 s1 = unpair(s2), t1 = unpair(t2);
-    Sums sums = join_all(Sums{r, s1.x + s1.y, t1.x + t1.y, most, before});
+    Sums sums = join_all(Sums{r, s1.x + s1.y, t1.x + t1.y, most, before}, true);
     const bool far = fabsf(sums.most * c) >= kFar && fabsf(sums.most) < INFINITY;
     if (far) {
         // once more, with the maximum
@@ -504,17 +539,8 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         if (csize > 1) cluster_sync();   // the sums have been read
         __syncthreads();
         const int rank = sums.before;
-        sums = join_all(Sums{0.f, s, t, m, 0});
+        sums = join_all(Sums{0.f, s, t, m, 0}, false);
         sums.before = rank;
-    }
-    if (csize > 1 && TOP && crank == 0 && warp == 0) {
-        u64 best = top.best[lane];
-        for (int k = 1; k < csize; ++k) {
-            const float *other = (const float *)&top.best[lane];
-            const u64 key = (u64)__float_as_uint(cluster_load(other, k)) | (u64)__float_as_uint(cluster_load(other + 1, k)) << 32;
-            best = warp_merge(best, key, lane);
-        }
-        top.best[lane] = best;
     }
     if (crank == 0 && warp == 0) {
         // a row that holds a NaN has a NaN in s, one with a +inf gets it here
@@ -638,12 +664,13 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
 
 template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
 {
-    // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least
+    // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least.
+    // Clusters do not fit the last 15 % of the places, and a second wave costs more (100 rows in
+    // fp32: 25 us with four CTAs, 37 with six; 320 rows in bf16: 43 with three, 46 with two)
     // (launches one after the other; 64 rows in fp32: 22 us with eight, 24 with four; one
     // row: 12.5 with eight, 14.5 with sixteen)
     const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 32ll / W * sm_count();
-    int cluster = 1;
-    while (cluster < 8 && p.rows * cluster * 2 <= slots && p.vocab >= 2 * cluster * 2 * tile) cluster *= 2;
+    const int cluster = (int)std::max(1ll, std::min({8ll, slots * 85 / 100 / p.rows, p.vocab / (2 * tile)}));
     return launch_clusters(k_token_logprobs<BF16, TOP, W>, dim3((unsigned)p.rows * cluster), dim3(W * 32), cluster, 0, s, p);
 }
 
