@@ -44,7 +44,9 @@ template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of 
 // with 152, 256, 304, 456 CTAs in all 26.5, 21.9, 25.7, 36 us.
 constexpr int kMinBlocks = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSplits = 512;  // the clusters' statistics fit the place of a head of 64
+constexpr int kMaxSplits = 512;
+// A cluster's sums of R rows in global memory, and their statistics once for each slice.
+constexpr int partial_floats(int D, int R) { return R * D + kMaxCluster * R * 4; }
 
 template <bool INT8> __device__ __forceinline__ void key_operands(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
@@ -89,8 +91,7 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_factor[R], s_bias[R];
     __shared__ float s_stat[kW][3][R];         // maximum, sum of rounded p, sum of p of each warp
-    __shared__ float s_total[3][R];            // the same of the CTA, read by the cluster
-    __shared__ float s_weight[kMaxCluster][R], s_joined[3][R];
+    __shared__ __align__(16) float4 s_total[R];   // the same of the CTA, read by the cluster
     __shared__ uint32_t s_last;
     const KvParams &c = p.c;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -153,19 +154,19 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
             to[u].block = block - column * page_blocks;
         }
     };
-    auto load = [&](int it, const Place (&from)[U]) {
+    auto load = [&](int it, const Place (&from)[U], float (&ks)[U], float (&vs)[U], bool (&ok)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int block = s_lo + (it * kW + warp) * U + u, page = from[u].page;
-            n_ok[u] = page >= 0 && page < c.pages;
-            if (!n_ok[u]) {
+            ok[u] = page >= 0 && page < c.pages;
+            if (!ok[u]) {
                 if (block < s_hi && c.err && lane == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
                 continue;
             }
             const long long ph = (long long)page * c.kv_heads + h;
             const long long at = (ph * c.page_tokens + from[u].block * 16) * D;
-            n_ks[u] = __ldg(c.k_scales + ph);
-            n_vs[u] = __ldg(c.v_scales + ph);
+            ks[u] = __ldg(c.k_scales + ph);
+            vs[u] = __ldg(c.v_scales + ph);
             const int pos = block * 16;
             const bool whole = pos >= lo && pos + 16 <= end;
             // tokens outside [lo, end) are not read: zeros take their place
@@ -201,10 +202,9 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
         fetch(0, first);
         fetch(1, second);
         fetch(2, n_place);
-        load(0, first);
+        load(0, first, ks, vs, ok);
         cp_async_commit();
-        advance();
-        load(1, second);
+        load(1, second, n_ks, n_vs, n_ok);
         cp_async_commit();
     }
 
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
             }
         }
         advance();
-        load(it + 2, n_place);   // into the slot just read, by the lane that read it
+        load(it + 2, n_place, n_ks, n_vs, n_ok);   // into the slot just read, by the lane that read it
         cp_async_commit();
         fetch(it + 3, n_place);
     }
@@ -449,20 +449,18 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
                 sums[(warp * R + r) * D + i / 8 * 128 + ((col * 8 + g) ^ (t * 8))] = o[m][i][e] * f[e % 2];
             }
     }
-    // Row r's statistics of several parties, joined; the weights of theirs.
-    auto join = [&](int r, int count, const float (*stat)[3][R], float *weights, float *joined) {
-        float most = stat[0][0][r], l = 0.f, e = 0.f;
-#pragma unroll 8
-        for (int k = 1; k < count; ++k) most = fmaxf(most, stat[k][0][r]);
-#pragma unroll 8
-        for (int k = 0; k < count; ++k) {
-            const float f = weight(stat[k][0][r], most);
-            l = fmaf(f, stat[k][1][r], l), e = fmaf(f, stat[k][2][r], e);
-            if (weights) weights[k * R + r] = f;
+    if (threadIdx.x < R) {
+        const int r = threadIdx.x;
+        float most = s_stat[0][0][r], l = 0.f, e = 0.f;
+#pragma unroll
+        for (int w = 1; w < kW; ++w) most = fmaxf(most, s_stat[w][0][r]);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            const float f = weight(s_stat[w][0][r], most);
+            l = fmaf(f, s_stat[w][1][r], l), e = fmaf(f, s_stat[w][2][r], e);
         }
-        joined[0] = most, joined[R] = l, joined[2 * R] = e;
-    };
-    if (threadIdx.x < R) join(threadIdx.x, kW, s_stat, nullptr, s_total[0] + threadIdx.x);
+        s_total[r] = make_float4(most, l, e, 0.f);
+    }
     __syncthreads();
     float4 *sums4 = (float4 *)sums;
     for (int i = threadIdx.x; i < live * D / 4; i += kW * 32) {
@@ -493,111 +491,102 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
     };
     if (csize == 1 && clusters == 1) {
         __syncthreads();
-        for (int i = threadIdx.x; i < live * D / 4; i += kW * 32) finish(i * 4 / D, i * 4 % D, sums4[i], s_total[1][i * 4 / D]);
-        if (threadIdx.x < live) finish_lse(threadIdx.x, s_total[0][threadIdx.x], s_total[2][threadIdx.x]);
+        for (int i = threadIdx.x; i < live * D / 4; i += kW * 32) finish(i * 4 / D, i * 4 % D, sums4[i], s_total[i * 4 / D].y);
+        if (threadIdx.x < live) finish_lse(threadIdx.x, s_total[threadIdx.x].x, s_total[threadIdx.x].z);
         return;
     }
 
     // Join the cluster: every CTA takes a slice of a row's words, [crank * width, + width).
-    float (*stat)[3][R] = (float (*)[3][R])(sums + R * D);   // of the parties, in the other warps' place
-    cluster_sync();
-    {
-        float x[kMaxCluster * 3 * R / (kW * 32) + 1];
+    // Each thread reads the CTAs' statistics of its row beside their sums, and weighs them itself.
+    struct Joined {
+        float4 v;
+        float most, l, e;
+    };
+    auto take = [&](Joined &j, const auto &stat, const auto &x) {   // parties that are not there: most = -inf, zeros
+        constexpr int N = sizeof(stat) / sizeof(float4);
+        float most = j.most;
 #pragma unroll
-        for (int k = 0; k < kMaxCluster * 3 * R / (kW * 32) + 1; ++k) {
-            const int i = threadIdx.x + k * kW * 32;
-            x[k] = i < csize * 3 * R ? cluster_load(&s_total[0][0] + i % (3 * R), i / (3 * R)) : 0.f;
-        }
+        for (int k = 0; k < N; ++k) most = fmaxf(most, stat[k].x);
+        const float f = weight(j.most, most);
+        j.v.x *= f, j.v.y *= f, j.v.z *= f, j.v.w *= f, j.l *= f, j.e *= f, j.most = most;
 #pragma unroll
-        for (int k = 0; k < kMaxCluster * 3 * R / (kW * 32) + 1; ++k) {
-            const int i = threadIdx.x + k * kW * 32;
-            if (i < csize * 3 * R) (&stat[0][0][0])[i] = x[k];
+        for (int k = 0; k < N; ++k) {
+            const float f = weight(stat[k].x, most);
+            j.v.x = fmaf(f, x[k].x, j.v.x), j.v.y = fmaf(f, x[k].y, j.v.y), j.v.z = fmaf(f, x[k].z, j.v.z), j.v.w = fmaf(f, x[k].w, j.v.w);
+            j.l = fmaf(f, stat[k].y, j.l), j.e = fmaf(f, stat[k].z, j.e);
         }
-    }
-    __syncthreads();
-    if (threadIdx.x < R) join(threadIdx.x, csize, stat, s_weight[0], s_joined[0] + threadIdx.x);
-    __syncthreads();
-    const int width = D / csize;
-    const long long stride = R * D + kMaxCluster * R * 3;   // of a cluster's sums in global memory
+    };
+    const Joined nothing = {make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f, 0.f};
+    const float4 absent = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    const int width = D / csize, quads = live * width / 4, row_shift = 31 - __clz(width / 4);
+    const long long stride = partial_floats(D, R);
     float *partial = p.partial + item * (p.splits / csize) * stride;
-    for (int i = threadIdx.x; i < live * width / 4; i += kW * 32) {
-        const int r = i * 4 / width, word = crank * width + i * 4 % width;
-        float4 x[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) x[k] = cluster_load4(sums + r * D + word, k < csize ? k : 0);
+    auto end_of = [&](int r, int word, bool first, const Joined &j) {
+        finish(r, word, j.v, j.l);
+        if (crank == 0 && first) finish_lse(r, j.most, j.e);
+    };
+    cluster_sync();
+    for (int i = threadIdx.x; i < quads; i += kW * 32) {
+        const int r = i >> row_shift, in_row = i - (r << row_shift), word = crank * width + in_row * 4;
+        float4 stat[kMaxCluster], x[kMaxCluster];
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
-            const float f = k < csize ? s_weight[k][r] : 0.f;
-            if (k < csize) v.x = fmaf(f, x[k].x, v.x), v.y = fmaf(f, x[k].y, v.y), v.z = fmaf(f, x[k].z, v.z), v.w = fmaf(f, x[k].w, v.w);
+            stat[k] = absent, x[k] = nothing.v;
+            if (k < csize) stat[k] = cluster_load4((const float *)(s_total + r), k), x[k] = cluster_load4(sums + r * D + word, k);
         }
-        if (clusters == 1)
-            finish(r, word, v, s_joined[1][r]);
-        else
-            *(float4 *)(partial + ck * stride + r * D + word) = v;
+        Joined j = nothing;
+        take(j, stat, x);
+        if (clusters == 1) {
+            end_of(r, word, in_row == 0, j);
+        } else {
+            *(float4 *)(partial + ck * stride + r * D + word) = j.v;
+            if (in_row == 0) *(float4 *)(partial + ck * stride + R * D + (crank * R + r) * 4) = make_float4(j.most, j.l, j.e, 0.f);
+        }
     }
     cluster_arrive();   // this CTA has read the others' sums
     if (clusters == 1) {
-        if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
         cluster_wait();   // the others may still be reading this CTA's
         return;
     }
-    for (int i = threadIdx.x; i < 3 * R; i += kW * 32) partial[ck * stride + R * D + crank * 3 * R + i] = s_joined[0][i];
 
-    // Join the clusters: the last one to arrive, per slice of columns, in the clusters' order.
-    __threadfence();
+    // Join the clusters: the last one to arrive, per slice of columns.  The barrier and the
+    // ticket's release carry this CTA's sums, its acquire and the barrier the others'.
     __syncthreads();
     if (threadIdx.x == 0) {
         uint32_t *ticket = p.tickets + item * kMaxCluster + crank;
         s_last = atom_add_acq_rel(ticket, 1) == (uint32_t)clusters - 1;
         if (s_last) *ticket = 0;
-        __threadfence();
     }
     __syncthreads();
     cluster_wait();   // the others may still be reading this CTA's sums
     if (!s_last) return;
-    // four words and every fourth cluster at a time, as the threads go; the first sums are on
-    // their way while the weights are found
-    constexpr int LANES = 4, FIRST = 10;
-    const int from = threadIdx.x % LANES, quads = live * width / 4;
-    auto source = [&](int i) { return partial + (i < quads ? i * 4 / width * D + crank * width + i * 4 % width : 0); };
-    float4 first[FIRST];
-    {
-        const float *src = source(threadIdx.x / LANES);
+    // `lanes` threads for four words, each with every lanes-th cluster, some at a time
+    constexpr int FEW = D == 256 ? 16 : 8;
+    int lanes = 1;
+    while (lanes < 32 && quads * lanes * 2 <= kW * 32) lanes *= 2;
+    const int from = threadIdx.x % lanes;
+    for (int q0 = 0; q0 < quads; q0 += kW * 32 / lanes) {
+        const int i = q0 + threadIdx.x / lanes, r = i < quads ? i >> row_shift : 0, in_row = i - (r << row_shift), word = crank * width + in_row * 4;
+        const float *src = partial + r * D + (i < quads ? word : 0), *src_stat = partial + R * D + (crank * R + r) * 4;
+        Joined j = nothing;
+        for (int k0 = from; k0 < clusters; k0 += FEW * lanes) {
+            float4 stat[FEW], x[FEW];
 #pragma unroll
-        for (int k = 0; k < FIRST; ++k)
-            first[k] = from + k * LANES < clusters ? __ldcg((const float4 *)(src + (from + k * LANES) * stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 8
-    for (int i = threadIdx.x; i < clusters * 3 * R; i += kW * 32)
-        (&stat[0][0][0])[i] = __ldcg(partial + i / (3 * R) * stride + R * D + crank * 3 * R + i % (3 * R));
-    float *weights = sums;   // [cluster][R]
-    __syncthreads();
-    if (threadIdx.x < R) join(threadIdx.x, clusters, stat, weights, s_joined[0] + threadIdx.x);
-    __syncthreads();
-    for (int q0 = 0; q0 < quads; q0 += kW * 32 / LANES) {
-        const int i = q0 + threadIdx.x / LANES, r = i < quads ? i * 4 / width : 0;
-        const float *src = source(i);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto take = [&](int k, const float4 &x) {
-            const float f = weights[k * R + r];
-            v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-        };
-        int k = from;
-        if (q0 == 0) {
-#pragma unroll
-            for (int j = 0; j < FIRST; ++j, k += LANES)
-                if (k < clusters) take(k, first[j]);
+            for (int k = 0; k < FEW; ++k) {
+                const int at = k0 + k * lanes;
+                stat[k] = absent, x[k] = nothing.v;
+                if (at < clusters) stat[k] = __ldcg((const float4 *)(src_stat + at * stride)), x[k] = __ldcg((const float4 *)(src + at * stride));
+            }
+            take(j, stat, x);
         }
-#pragma unroll 8
-        for (; k < clusters; k += LANES) take(k, __ldcg((const float4 *)(src + k * stride)));
-#pragma unroll
-        for (int o = 1; o < LANES; o *= 2) {
-            v.x += __shfl_xor_sync(~0u, v.x, o), v.y += __shfl_xor_sync(~0u, v.y, o);
-            v.z += __shfl_xor_sync(~0u, v.z, o), v.w += __shfl_xor_sync(~0u, v.w, o);
+        for (int o = 1; o < lanes; o *= 2) {
+            const float4 stat[1] = {make_float4(__shfl_xor_sync(~0u, j.most, o), __shfl_xor_sync(~0u, j.l, o), __shfl_xor_sync(~0u, j.e, o), 0.f)};
+            const float4 x[1] = {make_float4(__shfl_xor_sync(~0u, j.v.x, o), __shfl_xor_sync(~0u, j.v.y, o), __shfl_xor_sync(~0u, j.v.z, o),
+                                             __shfl_xor_sync(~0u, j.v.w, o))};
+            take(j, stat, x);
         }
-        if (i < quads && from == 0) finish(r, crank * width + i * 4 % width, v, s_joined[1][r]);
+        if (i < quads && from == 0) end_of(r, word, in_row == 0, j);
     }
-    if (crank == 0 && threadIdx.x < live) finish_lse(threadIdx.x, s_joined[0][threadIdx.x], s_joined[2][threadIdx.x]);
 }
 
 template <int D, bool INT8, int NT> cudaError_t launch(const KvAttentionParams &p, const KvAttentionPlan &plan, cudaStream_t s)
@@ -639,7 +628,7 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     if (plan.items * kMaxCluster > MTP_KV_WORKSPACE_ZEROED / 4) splits = plan.cluster;
     plan.splits = (int)splits;
     if (splits > plan.cluster)
-        plan.partial_floats = (size_t)plan.items * (splits / plan.cluster) * (R * c.dim + kMaxCluster * R * 3);
+        plan.partial_floats = (size_t)plan.items * (splits / plan.cluster) * partial_floats(c.dim, R);
     return plan;
 }
 
