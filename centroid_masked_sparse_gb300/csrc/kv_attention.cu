@@ -39,9 +39,9 @@ namespace {
 
 constexpr int kW = 4;            // warps of a CTA
 template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of codes of a step
-// Blocks of 16 tokens that a CTA should have at least.  A grid fills the GPU once or a little
-// more: the ragged sequences with 1, 2, 4, 8 CTAs an item 147, 141, 139, 171 us, the long one
-// with 152, 256, 304, 456 CTAs in all 26.5, 21.9, 25.7, 36 us.
+// Blocks of 16 tokens that a CTA should have at least (65519 tokens, D = 256: 128, 192, 256, 304,
+// 384 CTAs 24, 20.4, 17.1, 20.3, 18.8 us; 8191 tokens, 8 kv heads of 128: 16 blocks 10.6 us,
+// eight 11.5, 24 12).
 constexpr int kMinBlocks = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 512;
@@ -617,13 +617,24 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     const long long cap = (long long)c.table_width * c.page_tokens;
     long long seen = max_len > 0 ? std::min<long long>(max_len, cap) : cap;
     if (window > 0) seen = std::min(seen, window + longest_q - 1);
-    // four rounds of CTAs where there are many items, whose lengths may differ
-    const long long slots = (long long)sm_count() * ctas_per_sm(c.dim, plan.tiles8);
-    const long long most = (seen / 16 + kMinBlocks) / kMinBlocks;
-    long long splits = plan.items >= slots / 2 ? 4 * slots / plan.items : slots / plan.items;
+    const long long slots = (long long)sm_count() * ctas_per_sm(c.dim, plan.tiles8), blocks = seen / 16 + 1;
+    // CTAs of an item.  Alike items (one sequence, or a window of all): what fits at once, less
+    // the 3 % that whole clusters leave empty, or four rounds where even one each is half of
+    // that.  Unlike ones: one cluster each, in up to four rounds, or more clusters where a round
+    // and a third has room (32 heads on 8, D = 128, up to 8191 tokens: 8 sequences with 4, 8, 16,
+    // 24 CTAs an item 33, 24, 29, 29 us; 24 sequences with 2, 4, 8, 16: 70, 63, 59, 73 us; 4
+    // sequences with 8, 16, 24, 32: 18, 15.6, 14.8, 15.3 us; the window of 512, 64 items, with 2,
+    // 4, 8: 13.8, 12.8, 18.8 us).
+    const bool alike = c.batch == 1 || window > 0;
+    const long long fit = slots * 97 / 100 / plan.items, loose = slots * 13 / 10 / plan.items, rounds = 4 * slots / plan.items;
+    long long splits = alike ? (plan.items >= slots / 2 ? rounds : fit) : loose >= 16 ? loose : std::min(rounds, 8ll);
+    // at least kMinBlocks each; a first cluster costs little, so a block for each warp is
+    // enough for that where it fits at once
+    const long long most = std::max((blocks + kMinBlocks - 1) / kMinBlocks, std::min({8ll, fit, (blocks + kW - 1) / kW}));
     splits = std::max(1ll, std::min({splits, most, (long long)kMaxSplits}));
-    plan.cluster = splits >= 5 ? 8 : splits >= 3 ? 4 : (int)splits;
-    splits = (splits + plan.cluster - 1) / plan.cluster * plan.cluster;
+    const long long up = alike ? 0 : 1;
+    plan.cluster = splits >= 8 - 2 * up ? 8 : splits >= 4 - up ? 4 : splits >= 2 ? 2 : 1;
+    splits = std::max<long long>(plan.cluster, splits / plan.cluster * plan.cluster);
     // without tickets for every item there is one cluster for each
     if (plan.items * kMaxCluster > MTP_KV_WORKSPACE_ZEROED / 4) splits = plan.cluster;
     plan.splits = (int)splits;
