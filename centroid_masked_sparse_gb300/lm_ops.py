@@ -49,11 +49,13 @@ def _stream(stream, index):
     return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _vector(t, dtype, n, device):
-    """The address of a contiguous tensor of n elements on the call's GPU, or None."""
+# Calls of a few microseconds are all host: the wrappers compare types by identity (there is one object for each)
+# and GPUs by number, which take half the time of comparing torch's device objects.
+def _vector(t, dtype, n, where):
+    """The address of a contiguous tensor of n elements on the call's GPU (get_device()'s number), or None."""
     if t is None:
         return None
-    assert t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.device == device
+    assert t.dtype is dtype and t.numel() == n and t.get_device() == where and t.is_contiguous()
     return t.data_ptr()
 
 
@@ -76,7 +78,7 @@ class Q4Weight:
         assert scales.dim() == 2 and scales.shape[0] == codes.shape[0]
         assert zeros is None or (zeros.dtype == torch.uint8 and zeros.shape == scales.shape and zeros.is_contiguous()
                                  and zeros.device == codes.device)
-        self.device, self.index = codes.device, codes.device.index or 0
+        self.device, self.index, self.where = codes.device, codes.device.index or 0, codes.get_device()
         self.rows, self.cols = int(codes.shape[0]), 2 * int(codes.shape[1])
         self.group = self.cols // max(1, int(scales.shape[1]))
         assert self.group * int(scales.shape[1]) == self.cols, "scales do not divide the columns into groups"
@@ -110,19 +112,20 @@ def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
 def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, stream=None):
     """[B, M]: softcap(x @ w.T) of x bf16 [B, K], in fp32 or rounded once to bf16 (out's type, or out_dtype)."""
     batch, cols = x.shape
-    rows = weight.rows
-    assert x.dtype == torch.bfloat16 and cols == weight.cols and x.stride(1) == 1 and x.device == weight.device
+    rows, where = weight.rows, weight.where
+    x_strides = x.stride()
+    assert x.dtype is torch.bfloat16 and cols == weight.cols and x_strides[1] == 1 and x.get_device() == where
     if out is None:
         out = torch.empty(batch, rows, dtype=out_dtype, device=weight.device)
-    assert out.shape == (batch, rows) and (out.stride(1) == 1 or rows == 1) and out.device == weight.device
+    out_strides = out.stride()
+    assert out.shape == (batch, rows) and (out_strides[1] == 1 or rows == 1) and out.get_device() == where
     desc = weight.desc
     if softcap != 0.0:
         desc = MtpQ4Desc.from_buffer_copy(desc)
         desc.softcap = softcap
     many = batch > 1
-    check(lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), x.stride(0) if many else cols, batch, out.data_ptr(),
-                              _TYPES[out.dtype], out.stride(0) if many else rows, _stream(stream, weight.index)),
-          "mtp_q4_matvec")
+    check(lib().mtp_q4_matvec(desc, x.data_ptr(), x_strides[0] if many else cols, batch, out.data_ptr(), _TYPES[out.dtype],
+                              out_strides[0] if many else rows, _stream(stream, weight.index)), "mtp_q4_matvec")
     return out
 
 
@@ -145,9 +148,10 @@ class KvCache:
         assert len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) == 1
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.format, self.device, self.index = format, k_codes.device, k_codes.device.index or 0
+        self.where = k_codes.get_device()
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = (int(n) for n in k_codes.shape)
         self.errors = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._ws, self._needs = None, {}
+        self._ws, self._needs = {}, {}   # workspaces by stream, and what calls need by their sizes
         self.desc = MtpKvDesc(num_pages=self.pages, page_tokens=self.page_tokens, kv_heads=self.kv_heads,
                               head_dim=self.head_dim, format=_FORMATS[format], device=self.index,
                               k_codes=k_codes.data_ptr(), v_codes=v_codes.data_ptr(), k_scales=k_scales.data_ptr(),
@@ -164,11 +168,13 @@ class KvCache:
         return cls(codes(), codes(), scales(), scales(), format)
 
     def workspace(self, need, stream=None):
-        """A cached attention workspace of at least `need` bytes, zeroed on the call's stream when it is made."""
-        ws = self._ws
+        """A kept attention workspace of at least `need` bytes, one for each stream, since calls on two streams
+        may run at once; zeroed on its stream when it is made."""
+        key = _stream(stream, self.index)
+        ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
             with torch.cuda.stream(stream):
-                ws = self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+                ws = self._ws[key] = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return ws
 
     def read_errors(self):
@@ -180,13 +186,14 @@ class KvCache:
 
 def _batch_desc(cache, page_table, lengths, starts, tokens, max_tokens):
     batch, width = page_table.shape
-    device = cache.device
-    assert page_table.dtype == torch.int32 and page_table.device == device and (page_table.stride(1) == 1 or width == 1)
+    where, strides = cache.where, page_table.stride()
+    assert page_table.dtype is torch.int32 and page_table.get_device() == where and (strides[1] == 1 or width == 1)
     if max_tokens is None:
         assert starts is None, "ragged calls need the most tokens that one sequence brings"
         max_tokens = max(1, tokens // max(1, batch))
-    return MtpKvBatch(batch, tokens, max_tokens, width, page_table.data_ptr(), page_table.stride(0) if batch > 1 else width,
-                      _vector(lengths, torch.int32, batch, device), _vector(starts, torch.int32, batch + 1, device))
+    return MtpKvBatch(batch, tokens, max_tokens, width, page_table.data_ptr(), strides[0] if batch > 1 else width,
+                      _vector(lengths, torch.int32, batch, where),
+                      None if starts is None else _vector(starts, torch.int32, batch + 1, where))
 
 
 def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, stream=None) -> None:
@@ -194,14 +201,14 @@ def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, s
 
     page_table int32 [B, width], lengths int32 [B]; sequence b brings rows starts[b]..starts[b + 1] (int32
     [B + 1]; at most max_new of them), or without starts an equal share of the rows."""
-    shape, device = k.shape, cache.device
+    shape, where = k.shape, cache.where
     tokens, heads, dim = shape
     assert heads == cache.kv_heads and dim == cache.head_dim and v.shape == shape
-    assert k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16 and k.device == device and v.device == device
+    assert k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.get_device() == where and v.get_device() == where
     k_strides, v_strides = k.stride(), v.stride()
     assert k_strides[2] == 1 and v_strides[2] == 1
     seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_new)
-    check(lib().mtp_kv_append(ctypes.byref(cache.desc), ctypes.byref(seqs), k.data_ptr(), k_strides[0], k_strides[1],
+    check(lib().mtp_kv_append(cache.desc, seqs, k.data_ptr(), k_strides[0], k_strides[1],
                               v.data_ptr(), v_strides[0], v_strides[1], _stream(stream, cache.index)), "mtp_kv_append")
 
 
@@ -217,17 +224,17 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
     lengths are the tokens of each sequence in the cache, with the ones that q belongs to; starts and max_q as
     in mtp_kv_append; max_len bounds the lengths (0: the table's width); window 0 sees everything; scale is
     head_dim ** -0.5 unless given."""
-    shape, device = q.shape, cache.device
+    shape, where = q.shape, cache.where
     tokens, heads, dim = shape
     strides = q.stride()
-    assert q.dtype == torch.bfloat16 and dim == cache.head_dim and strides[2] == 1 and q.device == device
+    assert q.dtype is torch.bfloat16 and dim == cache.head_dim and strides[2] == 1 and q.get_device() == where
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     if lse is None:
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=device)
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=cache.device)
     assert out.shape == shape
     seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_q)
-    desc, library = ctypes.byref(cache.desc), lib()
+    desc, library = cache.desc, lib()
     if workspace is None:
         # what a call needs goes by its sizes
         key = (seqs.batch, tokens, seqs.max_tokens, seqs.table_width, starts is None, heads, max_len, window)
@@ -235,11 +242,11 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
         if need is None:
             if len(cache._needs) > 4096:
                 cache._needs.clear()
-            need = cache._needs[key] = library.mtp_kv_attention_workspace_bytes(desc, ctypes.byref(seqs), heads, max_len, window)
+            need = cache._needs[key] = library.mtp_kv_attention_workspace_bytes(desc, seqs, heads, max_len, window)
         workspace = cache.workspace(need, stream)
-    check(library.mtp_kv_attention(desc, ctypes.byref(seqs), q.data_ptr(), strides[0], strides[1], heads, max_len, window,
-                                   dim ** -0.5 if scale is None else scale, _vector(out, torch.bfloat16, out.numel(), device),
-                                   _vector(lse, torch.float32, tokens * heads, device), workspace.data_ptr(),
+    check(library.mtp_kv_attention(desc, seqs, q.data_ptr(), strides[0], strides[1], heads, max_len, window,
+                                   dim ** -0.5 if scale is None else scale, _vector(out, torch.bfloat16, tokens * heads * dim, where),
+                                   _vector(lse, torch.float32, tokens * heads, where), workspace.data_ptr(),
                                    workspace.numel(), _stream(stream, cache.index)), "mtp_kv_attention")
     return out, lse
 
@@ -270,20 +277,20 @@ def mtp_token_logprobs(logits, tokens, top=0, temperature=1.0, out=None, stream=
     """Log probability and rank of tokens[r] (int32 [rows]; outside the vocabulary: no token) in logits[r], the
     row's entropy and lse, and its `top` largest alternatives.  out: an earlier result to write into."""
     rows, vocab, ld = _rows(logits)
-    device = logits.device
+    where, kind = logits.get_device(), _TYPES[logits.dtype]
     f32, i32 = torch.float32, torch.int32
     if out is None:
         def empty(*shape, dtype=f32):
-            return torch.empty(*shape, dtype=dtype, device=device)
+            return torch.empty(*shape, dtype=dtype, device=logits.device)
         out = TokenLogprobs(empty(rows), empty(rows), empty(rows, dtype=i32), empty(rows),
                             empty(rows, top, dtype=i32) if top else None, empty(rows, top) if top else None)
     logprob, entropy, rank, lse, top_ids, top_logprobs = out
-    check(lib().mtp_token_logprobs(logits.data_ptr(), _TYPES[logits.dtype], ld, rows, vocab,
-                                   _vector(tokens, i32, rows, device), temperature, top,
-                                   _vector(logprob, f32, rows, device), _vector(entropy, f32, rows, device),
-                                   _vector(rank, i32, rows, device), _vector(lse, f32, rows, device),
-                                   _vector(top_ids, i32, rows * top, device), _vector(top_logprobs, f32, rows * top, device),
-                                   device.index, _stream(stream, device.index)), "mtp_token_logprobs")
+    check(lib().mtp_token_logprobs(logits.data_ptr(), kind, ld, rows, vocab,
+                                   _vector(tokens, i32, rows, where), temperature, top,
+                                   _vector(logprob, f32, rows, where), _vector(entropy, f32, rows, where),
+                                   _vector(rank, i32, rows, where), _vector(lse, f32, rows, where),
+                                   _vector(top_ids, i32, rows * top, where), _vector(top_logprobs, f32, rows * top, where),
+                                   where, _stream(stream, where)), "mtp_token_logprobs")
     return out
 
 
@@ -292,15 +299,15 @@ def mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with respect to the logits, in their
     type.  out may be the logits themselves."""
     rows, vocab, ld = _rows(logits)
-    device, f32 = logits.device, torch.float32
+    where, dtype, f32 = logits.get_device(), logits.dtype, torch.float32
     if out is None:
-        out = torch.empty(rows, vocab, dtype=logits.dtype, device=device)
+        out = torch.empty(rows, vocab, dtype=dtype, device=logits.device)
     out_rows, out_cols, ld_out = _rows(out)
-    assert out_rows == rows and out_cols == vocab and out.dtype == logits.dtype and out.device == device
+    assert out_rows == rows and out_cols == vocab and out.dtype is dtype and out.get_device() == where
     check(lib().mtp_token_logprobs_backward(
-        logits.data_ptr(), _TYPES[logits.dtype], ld, rows, vocab, _vector(tokens, torch.int32, rows, device), temperature,
-        _vector(lse, f32, rows, device), _vector(entropy, f32, rows, device), _vector(grad_logprob, f32, rows, device),
-        _vector(grad_entropy, f32, rows, device), out.data_ptr(), ld_out, device.index, _stream(stream, device.index)),
+        logits.data_ptr(), _TYPES[dtype], ld, rows, vocab, _vector(tokens, torch.int32, rows, where), temperature,
+        _vector(lse, f32, rows, where), _vector(entropy, f32, rows, where), _vector(grad_logprob, f32, rows, where),
+        _vector(grad_entropy, f32, rows, where), out.data_ptr(), ld_out, where, _stream(stream, where)),
         "mtp_token_logprobs_backward")
     return out
 

@@ -394,6 +394,27 @@ def test_attention_on_another_stream_and_repeated():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_attention_on_two_streams_at_once():
+    """Calls on two streams share nothing: each has its own workspace, and both give what a call alone gives."""
+    g = gen(21)
+    lengths = [9000, 60, 4000]
+    cache, table = make_cache(g, lengths, 2, 128, 32, "int8")
+    q = [randn(g, 3, 8, 128).to(BF16) for _ in range(2)]
+    lens = ints(lengths)
+    want = [mtp.mtp_kv_attention(cache, table, lens, x) for x in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = ([], [])
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(mtp.mtp_kv_attention(cache, table, lens, q[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 def test_attention_in_a_graph():
     g = gen(19)
     cache, table = make_cache(g, [3000, 77], 1, 64, 16, "e4m3")
