@@ -148,9 +148,7 @@ constexpr int kGroups = 32, kOvers = 64;
 template <int W> struct TopState {
     static constexpr int kKeys = W * 32 * 8;   // what one vector of every thread may bring
     union {
-        // the threads' largest logits by groups of tiles: bf16, rounded up; the padding spreads
-        // a thread's groups over the banks
-        unsigned short group[kGroups][W * 32 + 2];
+        unsigned short group[kGroups][W * 32];  // the threads' largest logits by groups of tiles: bf16, rounded up
         u64 cand[kKeys];
     };
     u64 lists[W][32];
@@ -249,11 +247,11 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     auto load = [&](int tile, uint4 (&v)[kVecs]) {
         if (tile < whole) {
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j) v[j] = ld_stream16(at_load + j * TH);
+            for (int j = 0; j < kVecs; ++j) v[j] = ld_ro16(at_load + j * TH);
         } else {
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
-                v[j] = (tile * kVecs + j) * TH + threadIdx.x < vecs ? ld_stream16(at_load + j * TH)
+                v[j] = (tile * kVecs + j) * TH + threadIdx.x < vecs ? ld_ro16(at_load + j * TH)
                                                                    : make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
         }
         at_load += kVecs * TH;
@@ -413,17 +411,19 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             if (behind_it && v_behind >= reach) push(v_behind, tail + threadIdx.x, 0);
         };
         if (in_group) top.group[groups++][threadIdx.x] = bf16_up(of_group);
-        // The groups that reach it: the warp looks at one thread's after the other, a lane each.
-        __syncwarp();
+        // The groups that reach it: each thread's as bits, then one of every thread at a time.
         const int each = group_tiles * kVecs;   // vectors of a group
+        uint32_t reached = 0;
+        if (__any_sync(~0u, most >= reach)) {
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k)
+                if (k < groups) reached |= (uint32_t)(bf_lo(top.group[k][threadIdx.x]) >= reach) << k;
+        }
         int overs = 0;
-        for (uint32_t left = __ballot_sync(~0u, most >= reach); left; left &= left - 1) {
-            const int who = warp * 32 + __ffs(left) - 1;
-            const bool reaches = lane < groups && bf_lo(top.group[lane][who]) >= reach;
-            const uint32_t all_reach = __ballot_sync(~0u, reaches);
-            const int at = overs + __popc(all_reach & ((1u << lane) - 1));
-            if (reaches && at < kOvers) top.over[warp][at] = (unsigned short)(lane * TH + who);
-            overs += __popc(all_reach);
+        for (uint32_t some; (some = __ballot_sync(~0u, reached != 0)) != 0; reached &= reached - 1) {
+            const int at = overs + __popc(some & ((1u << lane) - 1));
+            if (reached && at < kOvers) top.over[warp][at] = (unsigned short)((__ffs(reached) - 1) * TH + threadIdx.x);
+            overs += __popc(some);
         }
         if (overs > kOvers) top.many = 1, overs = 0;
         __syncwarp();
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
                     const int o = i / each, who = top.over[warp][o];
                     at[k] = (who / TH * each + i - o * each) * TH + who % TH;
                 }
-                if (at[k] < vecs) v[k] = ld_stream16((const uint4 *)base + at[k]);
+                if (at[k] < vecs) v[k] = ld_ro16((const uint4 *)base + at[k]);
             }
         };
         load_items(0);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
             u64 least = top.best[p.top - 1];   // the n-th best key so far
             for (int i0 = 0; i0 < vecs; i0 += TH) {
                 const int i = i0 + threadIdx.x;
-                if (i < vecs) look(ld_stream16((const uint4 *)base + i), i, least);
+                if (i < vecs) look(ld_ro16((const uint4 *)base + i), i, least);
                 __syncthreads();
                 if (top.have > 0) {
                     reduce_buffer(top, warp, lane);
