@@ -40,13 +40,12 @@ struct Q4Plan {
     int chunk;      // columns of x in shared memory at a time, a multiple of kCols
 };
 
-constexpr int kTiles = 2;    // row tiles of a warp that share one read of x
 constexpr int kCols = 256;   // columns of a step: 4 blocks of 64
 
 // Bytes of a tile's scales and zero points in a step, and of a ring slot.
 template <int GROUP> constexpr int kScales = 8 * (kCols / GROUP) * 4;
 template <int GROUP> constexpr int kZeros = kScales<GROUP> / 2;
-template <int GROUP, bool ZEROS> constexpr int kStage = kTiles * (2048 + kScales<GROUP> + (ZEROS ? kZeros<GROUP> : 0));
+template <int GROUP, bool ZEROS, int TILES> constexpr int kStage = TILES * (2048 + kScales<GROUP> + (ZEROS ? kZeros<GROUP> : 0));
 
 // Byte b of v (below 16) as a float: or-ed into 2^23, whose last place is 1.
 template <int B> __device__ __forceinline__ float byte_value(uint32_t v)
@@ -55,13 +54,13 @@ template <int B> __device__ __forceinline__ float byte_value(uint32_t v)
 }
 
 // NT: batch rows / 8; GROUP: columns of a group; ZEROS: zero points; W: warps; S: slots of a
-// warp's ring.
-template <int NT, int GROUP, bool ZEROS, int W, int S>
+// warp's ring; TILES: row tiles of a warp that share one read of x.
+template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES>
 __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan)
 {
     constexpr int WORDS = GROUP / 32;      // words of a lane in a group
     constexpr int SG = kCols / GROUP;      // groups of a step
-    constexpr int STAGE = kStage<GROUP, ZEROS>, SCALES = kScales<GROUP>, ZPS = kZeros<GROUP>;
+    constexpr int STAGE = kStage<GROUP, ZEROS, TILES>, SCALES = kScales<GROUP>, ZPS = kZeros<GROUP>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_factor[NT * 8], s_inverse[NT * 8];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -72,13 +71,13 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     float *xw = (float *)(xs + plan.chunk / 32 * NT * 32);                   // [word][NT * 8] sums of 32 columns
     const int blocks = p.blocks, all_steps = (p.K + kCols - 1) / kCols;
 
-    // tiles of this CTA, then of this warp.  Its work is a list of rounds (kTiles tiles each),
+    // tiles of this CTA, then of this warp.  Its work is a list of rounds (TILES tiles each),
     // each over all chunks of x; every warp of the CTA runs the same rounds and chunks.
     const int c_lo = (int)((long long)plan.tiles * blockIdx.x / gridDim.x);
     const int c_n = (int)((long long)plan.tiles * (blockIdx.x + 1) / gridDim.x) - c_lo;
     const int row_groups = W / plan.parts, rg = warp / plan.parts, part = warp % plan.parts;
     const int t_lo = c_lo + c_n * rg / row_groups, t_hi = c_lo + c_n * (rg + 1) / row_groups;
-    const int rounds = ((c_n + row_groups - 1) / row_groups + kTiles - 1) / kTiles;
+    const int rounds = ((c_n + row_groups - 1) / row_groups + TILES - 1) / TILES;
     const int chunk_steps = plan.chunk / kCols, chunks = (p.K + plan.chunk - 1) / plan.chunk;
     // steps [lo, hi) of chunk c that are this warp's
     auto share = [&](int c, int *lo, int *hi) {
@@ -92,23 +91,23 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     share(0, &l_k, &l_hi);
     auto load = [&](int slot) {
         while (l_tile < t_hi && l_k >= l_hi) {   // the next chunk or round with steps of this warp
-            if (++l_chunk == chunks) l_chunk = 0, l_tile += kTiles;
+            if (++l_chunk == chunks) l_chunk = 0, l_tile += TILES;
             share(l_chunk, &l_k, &l_hi);
         }
         if (l_tile >= t_hi) return;
         const int n = min(blocks - l_k * 4, 4);
         const uint32_t dst = ring_s + slot * STAGE;
 #pragma unroll
-        for (int r = 0; r < kTiles; ++r) {
+        for (int r = 0; r < TILES; ++r) {
             if (l_tile + r >= t_hi) break;
             const uint8_t *src = p.codes + ((long long)(l_tile + r) * blocks + l_k * 4) * 512 + lane * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < n) cp_async16(dst + r * 2048 + i * 512, src + i * 512);
             const long long at = (long long)(l_tile + r) * all_steps + l_k;
-            if (lane < SCALES / 16) cp_async16(dst + kTiles * 2048 + r * SCALES, p.scales + at * SCALES + lane * 16);
+            if (lane < SCALES / 16) cp_async16(dst + TILES * 2048 + r * SCALES, p.scales + at * SCALES + lane * 16);
             if (ZEROS && lane < ZPS / 16)
-                cp_async16(dst + kTiles * (2048 + SCALES) + r * ZPS, p.zeros + at * ZPS + lane * 16);
+                cp_async16(dst + TILES * (2048 + SCALES) + r * ZPS, p.zeros + at * ZPS + lane * 16);
         }
         ++l_k;
     };
@@ -185,9 +184,9 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     }
     __syncthreads();
 
-    float acc[kTiles][NT][4];
+    float acc[TILES][NT][4];
 #pragma unroll
-    for (int r = 0; r < kTiles; ++r)
+    for (int r = 0; r < TILES; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
 
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
 
     int slot = 0;
     for (int round = 0; round < rounds; ++round) {
-        const int tile = t_lo + round * kTiles, live = min(t_hi - tile, kTiles);
+        const int tile = t_lo + round * TILES, live = min(t_hi - tile, TILES);
         for (int c = 0; c < chunks; ++c) {
             if (round + c > 0 && chunks > 1) {
                 __syncthreads();
@@ -219,8 +218,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
                 load(slot == 0 ? S - 1 : slot - 1);
                 cp_async_commit();
                 const uint8_t *codes = ring + slot * STAGE + lane * 16;
-                const uint8_t *scales = ring + slot * STAGE + kTiles * 2048 + g * SG * 4;
-                const uint8_t *zeros = ring + slot * STAGE + kTiles * (2048 + SCALES) + g * SG * 2;
+                const uint8_t *scales = ring + slot * STAGE + TILES * 2048 + g * SG * 4;
+                const uint8_t *zeros = ring + slot * STAGE + TILES * (2048 + SCALES) + g * SG * 2;
                 slot = slot == S - 1 ? 0 : slot + 1;
                 const int word0 = k * (kCols / 32) - c * (plan.chunk / 32);
                 const uint4 *xk = xs + word0 * NT * 32;
@@ -230,14 +229,14 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
                 // zeros of x with scales of zero.
 #pragma unroll
                 for (int j = 0; j < SG; ++j) {
-                    float d[kTiles][NT][4];
+                    float d[TILES][NT][4];
 #pragma unroll
                     for (int w = j * WORDS; w < (j + 1) * WORDS; ++w) {
                         uint4 x[NT];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) x[n] = xk[(w * NT + n) * 32 + ((g ^ w) * 4 + t)];
 #pragma unroll
-                        for (int r = 0; r < kTiles; ++r) {
+                        for (int r = 0; r < TILES; ++r) {
                             // words of rows g and g + 8: a block holds two words of each
                             const uint4 block = *(const uint4 *)(codes + r * 2048 + w / 2 * 512);
                             const uint32_t lo = w % 2 ? block.z : block.x, hi = w % 2 ? block.w : block.y;
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
 #pragma unroll
                     for (int n = 0; n < NT; ++n) sum[n] = *(const float2 *)(sk + (j * WORDS * NT + n) * 8);
 #pragma unroll
-                    for (int r = 0; r < kTiles; ++r) {
+                    for (int r = 0; r < TILES; ++r) {
                         const uint32_t s2 = *(const uint32_t *)(scales + r * SCALES + j * 4);
                         const float s_lo = bf_lo(s2), s_hi = bf_hi(s2);
                         float z_lo = s_lo, z_hi = s_hi;   // 8 is in the sums of x
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         }
         if (plan.parts == 1) {
 #pragma unroll
-            for (int r = 0; r < kTiles; ++r) {
+            for (int r = 0; r < TILES; ++r) {
                 if (r >= live) break;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -314,46 +313,47 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
 }
 
 // Columns of x that fit beside the rings of W warps of S slots.
-template <int NT, int GROUP, bool ZEROS, int W, int S> constexpr int q4_room()
+template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> constexpr int q4_room()
 {
-    constexpr long long left = 227 * 1024 - NT * 64 - (long long)W * S * kStage<GROUP, ZEROS>;
+    constexpr long long left = 227 * 1024 - NT * 64 - (long long)W * S * kStage<GROUP, ZEROS, TILES>;
     static_assert(left >= NT * 544 * kCols / 32, "a step of x fits");
-    static_assert(S * kStage<GROUP, ZEROS> >= NT * 512, "the parts' sums fit the rings");
+    static_assert(S * kStage<GROUP, ZEROS, TILES> >= NT * 512, "the parts' sums fit the rings");
     return (int)(left / (NT * 544) * 32 / kCols * kCols);   // 512 + 32 bytes per 32 columns and 8 rows
 }
 
-template <int NT, int GROUP, bool ZEROS, int W, int S> cudaError_t launch_q4_warps(const Q4Params &p, Q4Plan plan, cudaStream_t s)
+template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> cudaError_t launch_q4_warps(const Q4Params &p, Q4Plan plan, cudaStream_t s)
 {
     // all of x in shared memory, or in chunks that every CTA goes through for each round
-    plan.chunk = std::min((p.K + kCols - 1) / kCols * kCols, q4_room<NT, GROUP, ZEROS, W, S>());
-    const size_t smem = (size_t)W * S * kStage<GROUP, ZEROS> + (size_t)plan.chunk / 32 * NT * 544;
-    cudaError_t e = allow_smem((const void *)k_q4_matvec<NT, GROUP, ZEROS, W, S>, smem);
+    plan.chunk = std::min((p.K + kCols - 1) / kCols * kCols, q4_room<NT, GROUP, ZEROS, W, S, TILES>());
+    const size_t smem = (size_t)W * S * kStage<GROUP, ZEROS, TILES> + (size_t)plan.chunk / 32 * NT * 544;
+    cudaError_t e = allow_smem((const void *)k_q4_matvec<NT, GROUP, ZEROS, W, S, TILES>, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(std::min(sm_count(), plan.tiles), (p.B + NT * 8 - 1) / (NT * 8));
-    return launch_dependent(k_q4_matvec<NT, GROUP, ZEROS, W, S>, grid, dim3(W * 32), smem, s, p, plan);
+    return launch_dependent(k_q4_matvec<NT, GROUP, ZEROS, W, S, TILES>, grid, dim3(W * 32), smem, s, p, plan);
 }
 
-// 12 warps where each has more than a round of tiles, else 8, whose CTAs have less to set
-// up (launches one after the other; 262144 x 1536, 8 rows: 12 warps 43.3, 16 warps 45.5 us; 50021 x 2592, 23 rows: 43
-// with 12, 55 with 8, 53 with 16; 30000 x 2048, 8 rows: 14.6 with 12, 12.5 with 8, 16.7
-// with 16).  Three slots if x fits beside them (262144 x 1536, 8 rows: 45.3 with two).  With
-// x in chunks 8 warps are ahead up to 8 batch rows (65536 x 8192: 70 against 93 us), 12
-// above (90000 x 4096, 32 rows: 111 against 123).
+// 12 warps of two tiles where a CTA has more than 16 tiles, else 16 of one, which compute no
+// tile that is not there (8192 x 4096, 32 rows: 20.8 us, with 8 warps of two 29.4; 16384 x
+// 4096, one row: 11.1 and 15.2; 38000 x 2048, 8 rows, 16 tiles a CTA: 10.8 and 10.8).  Launches one
+// after the other: 262144 x 1536, 8 rows: 12 warps 43.3, 16 warps of two 45.5 us; 50021 x 2592,
+// 23 rows: 43 with 12, 55 with 8, 53 with 16.  Three slots if x fits beside them (262144 x
+// 1536, 8 rows: 45.3 with two).  With x in chunks 8 warps are ahead up to 8 batch rows (65536 x
+// 8192: 70 against 93 us), 12 above (90000 x 4096, 32 rows: 111 against 123).
 template <int NT, int GROUP, bool ZEROS> cudaError_t launch_q4(const Q4Params &p, cudaStream_t s)
 {
     Q4Plan plan{};
     plan.tiles = p.M / 16 + (p.M % 16 != 0);
     plan.parts = 1;
     const int sms = sm_count(), per_cta = (plan.tiles + sms - 1) / sms;
-    if (per_cta > 8 * kTiles) {
-        if (p.K <= q4_room<NT, GROUP, ZEROS, 12, 3>()) return launch_q4_warps<NT, GROUP, ZEROS, 12, 3>(p, plan, s);
-        if (NT > 1 || p.K <= q4_room<NT, GROUP, ZEROS, 12, 2>())
-            return launch_q4_warps<NT, GROUP, ZEROS, 12, 2>(p, plan, s);
+    if (per_cta > 16) {
+        if (p.K <= q4_room<NT, GROUP, ZEROS, 12, 3, 2>()) return launch_q4_warps<NT, GROUP, ZEROS, 12, 3, 2>(p, plan, s);
+        if (NT > 1 || p.K <= q4_room<NT, GROUP, ZEROS, 12, 2, 2>())
+            return launch_q4_warps<NT, GROUP, ZEROS, 12, 2, 2>(p, plan, s);
+        if constexpr (NT == 1) return launch_q4_warps<NT, GROUP, ZEROS, 8, 3, 2>(p, plan, s);
     }
-    // few tiles per CTA: its warps share the rows' columns instead, as long as each then has
-    // one tile at most
-    while (per_cta * plan.parts * 2 <= 8) plan.parts *= 2;
-    return launch_q4_warps<NT, GROUP, ZEROS, 8, 3>(p, plan, s);
+    // few tiles per CTA: its warps have one each, or share a row's columns
+    while (per_cta * plan.parts * 2 <= 16) plan.parts *= 2;
+    return launch_q4_warps<NT, GROUP, ZEROS, 16, 3, 1>(p, plan, s);
 }
 
 template <int NT, int GROUP> cudaError_t launch_q4_zeros(const Q4Params &p, cudaStream_t s)
