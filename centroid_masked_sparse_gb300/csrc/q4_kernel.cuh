@@ -36,7 +36,6 @@ namespace {
 
 struct Q4Plan {
     int tiles;      // tiles of 16 rows in all
-    int parts;      // warps that share a row's columns
     int chunk;      // columns of x in shared memory at a time, a multiple of kCols
 };
 
@@ -71,35 +70,54 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     float *xw = (float *)(xs + plan.chunk / 32 * NT * 32);                   // [word][NT * 8] sums of 32 columns
     const int blocks = p.blocks, all_steps = (p.K + kCols - 1) / kCols;
 
-    // tiles of this CTA, then of this warp.  Its work is a list of rounds (TILES tiles each),
-    // each over all chunks of x; every warp of the CTA runs the same rounds and chunks.
+    // Tiles of this CTA; x in chunks of columns.  With TILES = 2 a warp's work is a list of
+    // rounds (two tiles each), each over all chunks; every warp of the CTA runs the same rounds
+    // and chunks.  With TILES = 1 the CTA has at most a tile for each warp.  Up to 16 batch rows
+    // (TWO) each chunk's steps of all tiles, one tile after the other, are shared evenly: a warp
+    // has steps of tile t0 (of the CTA's) and perhaps of the next (21488 x 3392, 9 tiles a CTA, 5
+    // rows: 13 us, 17 with a tile for each warp).  Above, where a second tile's
+    // sums would not stay in registers (2048 x 4096, 32 rows: 16.5 us, without 14.8), `parts`
+    // warps share each tile's steps.
+    constexpr bool SPREAD = TILES == 1, TWO = SPREAD && NT <= 2;
     const int c_lo = (int)((long long)plan.tiles * blockIdx.x / gridDim.x);
     const int c_n = (int)((long long)plan.tiles * (blockIdx.x + 1) / gridDim.x) - c_lo;
-    const int row_groups = W / plan.parts, rg = warp / plan.parts, part = warp % plan.parts;
-    const int t_lo = c_lo + c_n * rg / row_groups, t_hi = c_lo + c_n * (rg + 1) / row_groups;
-    const int rounds = ((c_n + row_groups - 1) / row_groups + TILES - 1) / TILES;
+    int parts = 1;
+    if (SPREAD && !TWO)
+        while (c_n * parts * 2 <= W) parts *= 2;
+    const int t0 = SPREAD && !TWO ? warp / parts : c_n * warp / W;
+    const int t_lo = c_lo + t0, t_hi = c_lo + c_n * (warp + 1) / W;   // the latter with TILES = 2
+    const int rounds = SPREAD ? 1 : ((c_n + W - 1) / W + TILES - 1) / TILES;
     const int chunk_steps = plan.chunk / kCols, chunks = (p.K + plan.chunk - 1) / plan.chunk;
-    // steps [lo, hi) of chunk c that are this warp's
-    auto share = [&](int c, int *lo, int *hi) {
-        const int first = c * chunk_steps, n = min(chunk_steps, all_steps - first);
-        *lo = first + n * part / plan.parts;
-        *hi = first + n * (part + 1) / plan.parts;
+    // this warp's steps of chunk c: from step *k of tile t0 on, *n of them; the chunk ends at *end
+    auto share = [&](int c, int *k, int *n, int *end) {
+        const int first = c * chunk_steps, steps = min(chunk_steps, all_steps - first);
+        int lo = 0, hi = steps;
+        if (TWO)
+            lo = c_n * steps * warp / W - t0 * steps, hi = c_n * steps * (warp + 1) / W - t0 * steps;
+        else if (SPREAD)
+            lo = steps * (warp % parts) / parts, hi = t0 < c_n ? steps * (warp % parts + 1) / parts : lo;
+        *k = first + lo, *n = hi - lo, *end = first + steps;
     };
 
     // loads run ahead of the products through the same list
-    int l_tile = t_lo, l_chunk = 0, l_k, l_hi;
-    share(0, &l_k, &l_hi);
+    int l_tile = t_lo, l_chunk = 0, l_k, l_n, l_end;
+    share(0, &l_k, &l_n, &l_end);
+    if (!SPREAD && t_lo >= t_hi) l_n = 0, l_chunk = chunks;
     auto load = [&](int slot) {
-        while (l_tile < t_hi && l_k >= l_hi) {   // the next chunk or round with steps of this warp
-            if (++l_chunk == chunks) l_chunk = 0, l_tile += TILES;
-            share(l_chunk, &l_k, &l_hi);
+        while (l_n == 0) {   // the next chunk or round with steps of this warp
+            if (l_chunk == chunks) return;
+            if (++l_chunk == chunks) {
+                if (SPREAD || (l_tile += TILES) >= t_hi) return;
+                l_chunk = 0;
+            }
+            if (TWO) l_tile = t_lo;
+            share(l_chunk, &l_k, &l_n, &l_end);
         }
-        if (l_tile >= t_hi) return;
         const int n = min(blocks - l_k * 4, 4);
         const uint32_t dst = ring_s + slot * STAGE;
 #pragma unroll
         for (int r = 0; r < TILES; ++r) {
-            if (l_tile + r >= t_hi) break;
+            if (!SPREAD && l_tile + r >= t_hi) break;
             const uint8_t *src = p.codes + ((long long)(l_tile + r) * blocks + l_k * 4) * 512 + lane * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -109,7 +127,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
             if (ZEROS && lane < ZPS / 16)
                 cp_async16(dst + TILES * (2048 + SCALES) + r * ZPS, p.zeros + at * ZPS + lane * 16);
         }
-        ++l_k;
+        --l_n;
+        if (++l_k == l_end && TWO) l_k = l_chunk * chunk_steps, ++l_tile;
     };
     let_next_start();
     wait_for_previous();
@@ -184,9 +203,10 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     }
     __syncthreads();
 
-    float acc[TILES][NT][4];
+    constexpr int ACCS = TILES == 2 || TWO ? 2 : 1;
+    float acc[ACCS][NT][4];   // of the tiles at hand: both, or the one that is computed and the other
 #pragma unroll
-    for (int r = 0; r < TILES; ++r)
+    for (int r = 0; r < ACCS; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
 
@@ -209,74 +229,89 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
                 for (int n = warp; n < NT * 8; n += W) stage_x(c, n, 0);
                 __syncthreads();
             }
-            int k, k_hi;
-            share(c, &k, &k_hi);
-            if (live <= 0) k = k_hi;
-            for (; k < k_hi; ++k) {
-                cp_async_wait<S - 2>();
-                __syncwarp();   // the step is there for every lane, and the slot of the one before is free
-                load(slot == 0 ? S - 1 : slot - 1);
-                cp_async_commit();
-                const uint8_t *codes = ring + slot * STAGE + lane * 16;
-                const uint8_t *scales = ring + slot * STAGE + TILES * 2048 + g * SG * 4;
-                const uint8_t *zeros = ring + slot * STAGE + TILES * (2048 + SCALES) + g * SG * 2;
-                slot = slot == S - 1 ? 0 : slot + 1;
-                const int word0 = k * (kCols / 32) - c * (plan.chunk / 32);
-                const uint4 *xk = xs + word0 * NT * 32;
-                const float *sk = xw + word0 * NT * 8 + t * 2;
-                // No branch in here: a tile that is not there and columns beyond K are computed
-                // too, the one on whatever the slot holds (and not stored), the others on
-                // zeros of x with scales of zero.
+            int k, n_steps, end;
+            share(c, &k, &n_steps, &end);
+            if (!SPREAD && live <= 0) n_steps = 0;
+#pragma unroll 1
+            for (int part = 0; part < (TWO ? 2 : 1); ++part) {
+                const int k_hi = TWO ? min(end, k + n_steps) : k + n_steps;
+                n_steps -= k_hi - k;
+                for (; k < k_hi; ++k) {
+                    cp_async_wait<S - 2>();
+                    __syncwarp();   // the step is there for every lane, and the slot of the one before is free
+                    load(slot == 0 ? S - 1 : slot - 1);
+                    cp_async_commit();
+                    const uint8_t *codes = ring + slot * STAGE + lane * 16;
+                    const uint8_t *scales = ring + slot * STAGE + TILES * 2048 + g * SG * 4;
+                    const uint8_t *zeros = ring + slot * STAGE + TILES * (2048 + SCALES) + g * SG * 2;
+                    slot = slot == S - 1 ? 0 : slot + 1;
+                    const int word0 = k * (kCols / 32) - c * (plan.chunk / 32);
+                    const uint4 *xk = xs + word0 * NT * 32;
+                    const float *sk = xw + word0 * NT * 8 + t * 2;
+                    // No branch in here: a tile that is not there and columns beyond K are computed
+                    // too, the one on whatever the slot holds (and not stored), the others on
+                    // zeros of x with scales of zero.
 #pragma unroll
-                for (int j = 0; j < SG; ++j) {
-                    float d[TILES][NT][4];
+                    for (int j = 0; j < SG; ++j) {
+                        float d[TILES][NT][4];
 #pragma unroll
-                    for (int w = j * WORDS; w < (j + 1) * WORDS; ++w) {
-                        uint4 x[NT];
+                        for (int w = j * WORDS; w < (j + 1) * WORDS; ++w) {
+                            uint4 x[NT];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) x[n] = xk[(w * NT + n) * 32 + ((g ^ w) * 4 + t)];
+                            for (int n = 0; n < NT; ++n) x[n] = xk[(w * NT + n) * 32 + ((g ^ w) * 4 + t)];
+#pragma unroll
+                            for (int r = 0; r < TILES; ++r) {
+                                // words of rows g and g + 8: a block holds two words of each
+                                const uint4 block = *(const uint4 *)(codes + r * 2048 + w / 2 * 512);
+                                const uint32_t lo = w % 2 ? block.z : block.x, hi = w % 2 ? block.w : block.y;
+                                const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    if (w == j * WORDS)
+                                        mma_f16_first(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
+                                    else
+                                        mma_f16(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
+                                }
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16(d[r][n], lo8 & 0x000f000fu, hi8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x00f000f0u, x[n].z, x[n].w);
+                            }
+                        }
+                        float2 sum[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) sum[n] = *(const float2 *)(sk + (j * WORDS * NT + n) * 8);
 #pragma unroll
                         for (int r = 0; r < TILES; ++r) {
-                            // words of rows g and g + 8: a block holds two words of each
-                            const uint4 block = *(const uint4 *)(codes + r * 2048 + w / 2 * 512);
-                            const uint32_t lo = w % 2 ? block.z : block.x, hi = w % 2 ? block.w : block.y;
-                            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                if (w == j * WORDS)
-                                    mma_f16_first(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
-                                else
-                                    mma_f16(d[r][n], lo & 0x000f000fu, hi & 0x000f000fu, lo & 0x00f000f0u, hi & 0x00f000f0u, x[n].x, x[n].y);
+                            const uint32_t s2 = *(const uint32_t *)(scales + r * SCALES + j * 4);
+                            const float s_lo = bf_lo(s2), s_hi = bf_hi(s2);
+                            float z_lo = s_lo, z_hi = s_hi;   // 8 is in the sums of x
+                            if (ZEROS) {
+                                const uint32_t z = *(const uint16_t *)(zeros + r * ZPS + j * 2);
+                                z_lo *= byte_value<0>(z), z_hi *= byte_value<1>(z);
                             }
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16(d[r][n], lo8 & 0x000f000fu, hi8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x00f000f0u, x[n].z, x[n].w);
-                        }
-                    }
-                    float2 sum[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) sum[n] = *(const float2 *)(sk + (j * WORDS * NT + n) * 8);
-#pragma unroll
-                    for (int r = 0; r < TILES; ++r) {
-                        const uint32_t s2 = *(const uint32_t *)(scales + r * SCALES + j * 4);
-                        const float s_lo = bf_lo(s2), s_hi = bf_hi(s2);
-                        float z_lo = s_lo, z_hi = s_hi;   // 8 is in the sums of x
-                        if (ZEROS) {
-                            const uint32_t z = *(const uint16_t *)(zeros + r * ZPS + j * 2);
-                            z_lo *= byte_value<0>(z), z_hi *= byte_value<1>(z);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            fma_pair(acc[r][n][0], acc[r][n][1], s_lo, d[r][n][0], d[r][n][1]);
-                            fma_pair(acc[r][n][2], acc[r][n][3], s_hi, d[r][n][2], d[r][n][3]);
-                            fma_pair(acc[r][n][0], acc[r][n][1], z_lo, sum[n].x, sum[n].y);
-                            fma_pair(acc[r][n][2], acc[r][n][3], z_hi, sum[n].x, sum[n].y);
+                            for (int n = 0; n < NT; ++n) {
+                                fma_pair(acc[r][n][0], acc[r][n][1], s_lo, d[r][n][0], d[r][n][1]);
+                                fma_pair(acc[r][n][2], acc[r][n][3], s_hi, d[r][n][2], d[r][n][3]);
+                                fma_pair(acc[r][n][0], acc[r][n][1], z_lo, sum[n].x, sum[n].y);
+                                fma_pair(acc[r][n][2], acc[r][n][3], z_hi, sum[n].x, sum[n].y);
+                            }
                         }
                     }
                 }
+                if (TWO) {   // the rest is of the next tile
+                    k = c * chunk_steps;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float other = acc[0][n][e];
+                            acc[0][n][e] = acc[ACCS - 1][n][e], acc[ACCS - 1][n][e] = other;
+                        }
+                }
             }
         }
-        if (plan.parts == 1) {
+        if (!SPREAD) {
 #pragma unroll
             for (int r = 0; r < TILES; ++r) {
                 if (r >= live) break;
@@ -290,25 +325,30 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
             }
         }
     }
-    if (plan.parts == 1) return;
+    if (!SPREAD) return;
 
-    // the parts of each row are added in their order; a row group has one tile here.  The
-    // sums take the rings' place.
+    // each tile's sums, added in the order of the warps; they take the rings' place
     cp_async_wait<0>();
     __syncthreads();
-    float4 *sums = (float4 *)smem;   // [warp][NT][lane]
-    const int tiles = t_hi - t_lo;
+    float4 *sums = (float4 *)smem;   // [warp][its tiles][NT][lane]
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sums[(warp * NT + n) * 32 + lane] = make_float4(acc[0][n][0], acc[0][n][1], acc[0][n][2], acc[0][n][3]);
+    for (int r = 0; r < ACCS; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            sums[((warp * ACCS + r) * NT + n) * 32 + lane] = make_float4(acc[r][n][0], acc[r][n][1], acc[r][n][2], acc[r][n][3]);
     __syncthreads();
-    for (int n = part; n < tiles * NT; n += plan.parts) {
+    for (int i = warp; i < c_n * NT; i += W) {
+        const int tile = i / NT, n = i - tile * NT;
+        const int w_lo = TWO ? tile * W / c_n : tile * parts, w_hi = TWO ? ((tile + 1) * W - 1) / c_n : w_lo + parts - 1;
         float y[4] = {};
-        for (int q = 0; q < plan.parts; ++q) {
-            const float4 v = sums[((rg * plan.parts + q) * NT + n) * 32 + lane];
+#pragma unroll 4
+        for (int w = w_lo; w <= w_hi; ++w) {
+            const int r = TWO ? tile - c_n * w / W : 0;   // 0 or 1
+            const float4 v = sums[((w * ACCS + r) * NT + n) * 32 + lane];
             y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) store(y[e], t_lo * 16 + g + e / 2 * 8, n * 8 + t * 2 + e % 2);
+        for (int e = 0; e < 4; ++e) store(y[e], (c_lo + tile) * 16 + g + e / 2 * 8, n * 8 + t * 2 + e % 2);
     }
 }
 
@@ -317,7 +357,7 @@ template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> constexpr int 
 {
     constexpr long long left = 227 * 1024 - NT * 64 - (long long)W * S * kStage<GROUP, ZEROS, TILES>;
     static_assert(left >= NT * 544 * kCols / 32, "a step of x fits");
-    static_assert(S * kStage<GROUP, ZEROS, TILES> >= NT * 512, "the parts' sums fit the rings");
+    static_assert(TILES == 2 || S * kStage<GROUP, ZEROS, TILES> >= 2 * NT * 512, "the warps' sums fit the rings");
     return (int)(left / (NT * 544) * 32 / kCols * kCols);   // 512 + 32 bytes per 32 columns and 8 rows
 }
 
@@ -333,8 +373,8 @@ template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> cudaError_t la
 }
 
 // 12 warps of two tiles where a CTA has more than 16 tiles, else 16 of one, which compute no
-// tile that is not there (8192 x 4096, 32 rows: 20.8 us, with 8 warps of two 29.4; 16384 x
-// 4096, one row: 11.1 and 15.2; 38000 x 2048, 8 rows, 16 tiles a CTA: 10.8 and 10.8).  Launches one
+// tile that is not there (8192 x 4096, 32 rows: 21.5 us, with 8 warps of two 29.4; 16384 x
+// 4096, one row: 10.6 and 15.2; 38000 x 2048, 8 rows, 16 tiles a CTA: 11.0 and 10.8).  Launches one
 // after the other: 262144 x 1536, 8 rows: 12 warps 43.3, 16 warps of two 45.5 us; 50021 x 2592,
 // 23 rows: 43 with 12, 55 with 8, 53 with 16.  Three slots if x fits beside them (262144 x
 // 1536, 8 rows: 45.3 with two).  With x in chunks 8 warps are ahead up to 8 batch rows (65536 x
@@ -343,7 +383,6 @@ template <int NT, int GROUP, bool ZEROS> cudaError_t launch_q4(const Q4Params &p
 {
     Q4Plan plan{};
     plan.tiles = p.M / 16 + (p.M % 16 != 0);
-    plan.parts = 1;
     const int sms = sm_count(), per_cta = (plan.tiles + sms - 1) / sms;
     if (per_cta > 16) {
         if (p.K <= q4_room<NT, GROUP, ZEROS, 12, 3, 2>()) return launch_q4_warps<NT, GROUP, ZEROS, 12, 3, 2>(p, plan, s);
@@ -351,8 +390,6 @@ template <int NT, int GROUP, bool ZEROS> cudaError_t launch_q4(const Q4Params &p
             return launch_q4_warps<NT, GROUP, ZEROS, 12, 2, 2>(p, plan, s);
         if constexpr (NT == 1) return launch_q4_warps<NT, GROUP, ZEROS, 8, 3, 2>(p, plan, s);
     }
-    // few tiles per CTA: its warps have one each, or share a row's columns
-    while (per_cta * plan.parts * 2 <= 16) plan.parts *= 2;
     return launch_q4_warps<NT, GROUP, ZEROS, 16, 3, 1>(p, plan, s);
 }
 
