@@ -621,13 +621,16 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     // CTAs of an item.  Alike items (one sequence, or a window of all): what fits at once, less
     // the 3 % that whole clusters leave empty, or four rounds where even one each is half of
     // that.  Unlike ones: one cluster each, in up to four rounds, or more clusters where a round
-    // and a third has room (32 heads on 8, D = 128, up to 8191 tokens: 8 sequences with 4, 8, 16,
-    // 24 CTAs an item 33, 24, 29, 29 us; 24 sequences with 2, 4, 8, 16: 70, 63, 59, 73 us; 4
+    // and a quarter has room (32 heads on 8, D = 128, up to 8191 tokens: 8 sequences with 4, 8,
+    // 16, 24 CTAs an item 33, 24, 29, 29 us; 24 sequences with 2, 4, 8, 16: 70, 63, 59, 73 us; 4
     // sequences with 8, 16, 24, 32: 18, 15.6, 14.8, 15.3 us; the window of 512, 64 items, with 2,
-    // 4, 8: 13.8, 12.8, 18.8 us).
+    // 4, 8: 13.8, 12.8, 18.8 us).  At D = 256, whose joins are larger, clusters of four where
+    // these fill two thirds of the places (80 items of up to 4434 tokens with 2, 4, 8: 50, 40, 45
+    // us; 37 items of up to 5889 with 4, 8, 16: 36, 28, 33 us).
     const bool alike = c.batch == 1 || window > 0;
-    const long long fit = slots * 97 / 100 / plan.items, loose = slots * 13 / 10 / plan.items, rounds = 4 * slots / plan.items;
-    long long splits = alike ? (plan.items >= slots / 2 ? rounds : fit) : loose >= 16 ? loose : std::min(rounds, 8ll);
+    const long long fit = slots * 97 / 100 / plan.items, loose = slots * 5 / 4 / plan.items, rounds = 4 * slots / plan.items;
+    const long long one = c.dim == 256 && plan.items * 6 >= slots ? 4 : 8;
+    long long splits = alike ? (plan.items >= slots / 2 ? rounds : fit) : loose >= 16 ? loose : std::min(rounds, one);
     // at least kMinBlocks each; a first cluster costs little, so a block for each warp is
     // enough for that where it fits at once
     const long long most = std::max((blocks + kMinBlocks - 1) / kMinBlocks, std::min({8ll, fit, (blocks + kW - 1) / kW}));

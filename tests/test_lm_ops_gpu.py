@@ -70,6 +70,28 @@ def test_q4_matvec(rows, cols, group, zeros, batch, softcap, dtype):
     close(got, want, tol)
 
 
+# CTAs of 1 to 16 tiles (of 152), whose steps are shared among the warps, with x in one or several chunks
+@pytest.mark.parametrize("rows, cols, group, zeros, batch", [
+    (7000, 2048, 64, True, 8),
+    (9000, 6656, 64, False, 1),
+    (12000, 7936, 128, False, 13),
+    (21488, 3392, 64, True, 5),
+    (24320, 1024, 32, False, 16),
+    (38912, 320, 64, True, 3),
+    (20000, 4096, 32, False, 24),
+    (31000, 2304, 64, True, 31),
+])
+def test_q4_steps_shared_among_warps(rows, cols, group, zeros, batch):
+    g = gen(rows + batch)
+    codes, scales, points = q4_weight(g, rows, cols, group, zeros)
+    x = randn(g, batch, cols).to(BF16)
+    w = mtp.Q4Weight(codes, scales, points)
+    got = mtp.mtp_q4_matvec(w, x)
+    want, tol = ref.q4_matvec(codes, scales, points, group, x, 0.0, False)
+    close(got, want, tol)
+    assert torch.equal(mtp.mtp_q4_matvec(w, x), got)
+
+
 def test_q4_every_code_in_every_place():
     """Columns that each hold one code for one row: x is a unit vector, so each product is one exact weight."""
     g = gen(5)
