@@ -17,7 +17,7 @@
 // Both, times the group's scale, are added to the row's sum in fp32.
 //
 // What bounds it.  HBM up to 8 batch rows: 4.25 bits a weight with groups of 64; 262144 x
-// 1536 with 8 rows takes 39.8 us behind another launch, 5.6 TB/s, the same loads and stores
+// 1536 with 8 rows takes 39.3 us behind another launch, 5.7 TB/s, the same loads and stores
 // without the products about 2 us less.  Above, the products and what feeds them: 51.5 us at
 // 16 rows, 82.6 at 32; 50021 x 2592 with 23 rows takes 38 us with the tensor pipe 35 % busy,
 // one round of tiles a warp and x in two chunks.  Unpacking to bf16 with a subtraction of the
