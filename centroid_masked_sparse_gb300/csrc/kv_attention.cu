@@ -27,7 +27,7 @@
 // MB) take 131 us, 4.7 TB/s, with instructions in 0.44 of the issue slots and the tensor pipe
 // 13 % busy.  One sequence of 65519 tokens (one kv head of 256, 33.6 MB) takes 16.8 us: its
 // chain of look-ups, few steps and joins.  16 sequences of up to five query tokens in a window
-// of 512 take 12.7 us, 8 of them the host's call.  A warp per query row on the CUDA cores took
+// of 512 take 12.7 us, one pass through that chain.  A warp per query row on the CUDA cores took
 // 20.8 ms, 3 ms and 138 us.
 #include <algorithm>
 

@@ -19,8 +19,8 @@
 //
 // What bounds it: HBM for fp32; for bf16 instructions, 13 for two logits, although sums and
 // comparisons work on packed pairs: 320 rows of 262144 take 41.7 us with 20 alternatives, 4.0
-// TB/s, and 33.8 with none; in fp32 59 us, 5.7 TB/s.  One row takes 9 us: the host's call is
-// 7, the rest the cluster's joins.
+// TB/s, and 33.8 with none; in fp32 59 us, 5.7 TB/s.  One row takes 9 us, all
+// latency: a third of it its own reading, the rest the search and the joins of eight CTAs.
 #include <algorithm>
 #include <type_traits>
 
