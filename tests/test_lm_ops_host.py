@@ -131,6 +131,22 @@ def test_kv_attention_workspace(L):
     assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs()), 8, -1, 0) == 0
 
 
+def test_kv_attention_limits(L):
+    """Caches of more than 2^30 tokens a sequence and calls of more than 2^19 query rows are refused; workspaces follow
+    the split of every kind of call and are refused when they are short."""
+    def call(batch, heads=8, window=0, ws_bytes=1 << 40):
+        return L.mtp_kv_attention(ctypes.byref(kv()), ctypes.byref(batch), 0x80000, 1 << 20, 128, heads, 0, window, 0.1, 0x90000, None,
+                                  0xb0000, ws_bytes, None)
+    assert call(seqs(table_width=(1 << 25) + 1, ld_table=(1 << 25) + 1)) == UNSUPPORTED
+    assert call(seqs(batch=1, tokens=(1 << 16) + 1, max_tokens=(1 << 16) + 1)) == UNSUPPORTED
+    assert call(seqs(), heads=65536) == UNSUPPORTED
+    for batch in (seqs(batch=1, tokens=1, table_width=4096, ld_table=4096), seqs(batch=64, tokens=64), seqs(batch=3, tokens=9, max_tokens=7)):
+        for window in (0, 1, 100):
+            for max_len in (0, 1, 1 << 30):
+                assert L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(batch), 8, max_len, window) >= 262144
+            assert call(batch, window=window, ws_bytes=262143) == WORKSPACE
+
+
 @pytest.mark.parametrize("kw,expect", [
     (dict(type=2), UNSUPPORTED), (dict(rows=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(ld=999), SHAPE), (dict(temperature=0.0), SHAPE),
     (dict(temperature=-1.0), SHAPE), (dict(temperature=float("nan")), SHAPE), (dict(temperature=float("inf")), SHAPE),
