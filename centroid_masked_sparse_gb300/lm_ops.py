@@ -168,13 +168,21 @@ class KvCache:
         return cls(codes(), codes(), scales(), scales(), format)
 
     def workspace(self, need, stream=None):
-        """A kept attention workspace of at least `need` bytes, one for each stream, since calls on two streams
-        may run at once; zeroed on its stream when it is made."""
-        key = _stream(stream, self.index)
+        """An attention workspace of at least `need` bytes, zeroed on its stream when it is made.
+
+        One is kept for each stream, since calls on two streams may run at once.  A call that is being captured
+        gets one of its own from the graph's memory, with the zeroing in the graph: a kept one may not have been zeroed
+        yet when the graph runs, be in use beside it, or make way for a larger one.  Whoever captures can pass a workspace
+        (zeroed once, for one graph) to the call and spare the zeroing."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.workspace(need)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(need, dtype=torch.uint8, device=self.device)
+        key = _raw_stream(self.index)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
-            with torch.cuda.stream(stream):
-                ws = self._ws[key] = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            ws = self._ws[key] = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return ws
 
     def read_errors(self):

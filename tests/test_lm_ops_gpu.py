@@ -416,6 +416,30 @@ def test_attention_on_another_stream_and_repeated():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_attention_captured_without_a_call_before():
+    """Graphs own their workspaces: the second captured runs first, and eager calls that need more do not disturb them."""
+    g = gen(22)
+    lengths = [9000, 60, 4000]
+    cache, table = make_cache(g, lengths, 2, 128, 32, "int8")
+    q, lens = randn(g, 3, 8, 128).to(BF16), ints(lengths)
+    want = check_attention(cache, table, lengths, [1] * 3, q, uniform=True)
+    fresh = mtp.KvCache(cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, "int8")
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(mtp.mtp_kv_attention(fresh, table, lens, q))
+        graphs.append(graph)
+    many = randn(g, 24, 8, 128).to(BF16)
+    mtp.mtp_kv_attention(fresh, table, lens, q)
+    mtp.mtp_kv_attention(fresh, table, lens, many)
+    for k in (1, 0, 1, 0):
+        outs[k][0].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[k][0], want[0]) and torch.equal(outs[k][1], want[1])
+
+
 def test_attention_on_two_streams_at_once():
     """Calls on two streams share nothing: each has its own workspace, and both give what a call alone gives."""
     g = gen(21)
