@@ -569,10 +569,43 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     if (csize > 1) cluster_arrive(), cluster_wait();   // the first CTA may still be reading the others' lists
 }
 
-// grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))).  The logit of a masked
-// token is replaced by `low`, whose p is 0.  Bound by HBM: 1024 rows of 262144 bf16 take 159
-// us, 99 % of a copy's rate; 61 rows of 32003 6.6 us, the time of the host's call.
+// grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))), ln p_i = (x_i - m) factor - l.
+// m and l are 0 and lse, whose rounding is at most 2^-24 |lse| of p, where that stays below
+// kExactLse.  Beyond, fp32 has no room for l beside x factor (at -1e9, or with a row of nothing
+// but the type's lowest value, all of ln V is gone), so one CTA reads the row once more for its
+// maximum m and l = ln sum e^((x - m) factor), and writes all of it.  ln p is held at kNoWeight
+// from below, where p is 0, so that masked tokens and 0 * -inf need no branch.  Bound by HBM:
+// 1024 rows of 262144 bf16 take 159 us, 99 % of a copy's rate; 61 rows of 32003 6.6 us, the time
+// of the host's call.
 constexpr int kGradVecs = 4;   // vectors of a thread
+constexpr float kExactLse = 1024.f, kNoWeight = -1024.f;
+
+// The row's largest logit and the logarithm of its sum, for every thread of the CTA.
+template <bool BF16> __device__ __noinline__ float2 largest_and_sum(const typename Logits<BF16>::type *x, int vocab, float factor)
+{
+    __shared__ float s_most[kGradThreads / 32], s_sum[kGradThreads / 32];
+    const float c = factor * kLog2e;
+    float most = -INFINITY, sum = 0.f;
+    for (int i = threadIdx.x; i < vocab; i += kGradThreads) {
+        const float v = Logits<BF16>::value(x[i]);
+        if (v > most) {
+            sum *= exp2_fast((most - v) * c);   // 0 for the first
+            most = v;
+        }
+        sum += v == -INFINITY ? 0.f : exp2_fast((v - most) * c);
+    }
+    auto join = [&](float m, float s) {
+        const float up = fmaxf(most, m);
+        sum = (most == up ? sum : sum * exp2_fast((most - up) * c)) + (m == up ? s : s * exp2_fast((m - up) * c));
+        most = up;
+    };
+    for (int o = 16; o > 0; o >>= 1) join(__shfl_xor_sync(~0u, most, o), __shfl_xor_sync(~0u, sum, o));
+    if (threadIdx.x % 32 == 0) s_most[threadIdx.x / 32] = most, s_sum[threadIdx.x / 32] = sum;
+    __syncthreads();
+    most = s_most[0], sum = s_sum[0];
+    for (int w = 1; w < kGradThreads / 32; ++w) join(s_most[w], s_sum[w]);
+    return make_float2(most, logf(sum));
+}
 
 template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_backward(LogprobGradParams p)
 {
@@ -585,16 +618,34 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     T *g = (T *)p.grad + row * p.ld_grad;
     const int head = min(p.vocab, (int)((16 - ((uintptr_t)x & 15)) % 16 / sizeof(T)));
     const int vecs = (p.vocab - head) / VEC, tail = head + vecs * VEC;
-    const float low = lowest(p.factor);
-    const uint32_t low2 = bf16_bits(low) * 0x10001u;
     const bool together = (((uintptr_t)x ^ (uintptr_t)g) & 15) == 0;   // both on 16-byte boundaries at once
-    const float lse_in = __ldg(p.lse + row), lse = lse_in == -INFINITY ? 0.f : lse_in;   // nothing but masked tokens: all 0
+    constexpr int each = kGradVecs * kGradThreads;
+    uint4 in[kGradVecs];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int j = 0; j < kGradVecs; ++j) {
+            const int i = v0 + j * kGradThreads + threadIdx.x;
+            if (i < vecs) in[j] = __ldcs((const uint4 *)(x + head) + i);
+        }
+    };
+    load(blockIdx.y * each);
+    const float lse_in = __ldg(p.lse + row);
+    const bool far = fabsf(lse_in) >= kExactLse && lse_in != -INFINITY;
+    float most = 0.f, lse = lse_in == -INFINITY ? 0.f : lse_in;   // nothing but masked tokens: all 0
+    if (far) {
+        if (blockIdx.y > 0) return;
+        const float2 exact = largest_and_sum<BF16>(x, p.vocab, p.factor);   // every read is before the first write
+        most = exact.x, lse = exact.y;
+    }
+    const int stride = far ? each : gridDim.y * each;
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
     const float hot = p.grad_logprob && given >= 0 && given < p.vocab ? __ldg(p.grad_logprob + row) * p.factor : 0.f;
     const float ge = p.grad_entropy ? -__ldg(p.grad_entropy + row) * p.factor : 0.f;
     const float gl = (p.grad_entropy ? ge * __ldg(p.entropy + row) : 0.f) - hot;
     auto pair_of = [&](float a, float b) {   // the gradient of two logits, the given one's 1 apart
-        const u64 d = fma2(pair(a, b), pair(p.factor, p.factor), pair(-lse, -lse));
+        if (far) a -= most, b -= most;
+        const float2 l = unpair(fma2(pair(a, b), pair(p.factor, p.factor), pair(-lse, -lse)));
+        const u64 d = pair(max_nan(l.x, kNoWeight), max_nan(l.y, kNoWeight));
         const float2 e = unpair(mul2(d, pair(kLog2e, kLog2e)));
         return mul2(pair(exp2_fast(e.x), exp2_fast(e.y)), fma2(d, pair(ge, ge), pair(gl, gl)));
     };
@@ -606,7 +657,7 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     };
     auto one = [&](int i) {
         const float v = L::value(x[i]);
-        float r = unpair(pair_of(max_nan(v, low), 0.f)).x;
+        float r = unpair(pair_of(v, 0.f)).x;
         if (i == given && v != -INFINITY) r += hot;
         put(g + i, r);
     };
@@ -614,13 +665,7 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
         if (threadIdx.x < head) one(threadIdx.x);
         if (threadIdx.x < p.vocab - tail) one(tail + threadIdx.x);
     }
-    for (int v0 = blockIdx.y * kGradVecs * kGradThreads; v0 < vecs; v0 += gridDim.y * kGradVecs * kGradThreads) {
-        uint4 in[kGradVecs];
-#pragma unroll
-        for (int j = 0; j < kGradVecs; ++j) {
-            const int i = v0 + j * kGradThreads + threadIdx.x;
-            if (i < vecs) in[j] = __ldcs((const uint4 *)(x + head) + i);
-        }
+    for (int v0 = blockIdx.y * each; v0 < vecs; load(v0 += stride)) {
 #pragma unroll
         for (int j = 0; j < kGradVecs; ++j) {
             const int i = v0 + j * kGradThreads + threadIdx.x, id = head + i * VEC;
@@ -628,13 +673,7 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
             float r[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; e += 2) {
-                float2 u;
-                if (BF16) {
-                    const uint32_t w = max_nan_bf16x2(e == 0 ? in[j].x : e == 2 ? in[j].y : e == 4 ? in[j].z : in[j].w, low2);
-                    u = unpair(pair_of(bf_lo(w), bf_hi(w)));
-                } else {
-                    u = unpair(pair_of(max_nan(element<BF16>(in[j], e), low), max_nan(element<BF16>(in[j], e + 1), low)));
-                }
+                const float2 u = unpair(pair_of(element<BF16>(in[j], e), element<BF16>(in[j], e + 1)));
                 r[e] = u.x, r[e + 1] = u.y;
             }
             if (given >= id && given < id + VEC) {

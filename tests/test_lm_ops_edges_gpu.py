@@ -1,0 +1,80 @@
+"""The operators around the head on the GPU at the ends of their ranges: magnitudes, temperatures, lengths, bounds,
+strides, streams and what a query must not see, against 64-bit forms."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import centroid_masked_sparse_gb300 as mtp
+from tests import lm_ops_reference as ref
+from tests.test_lm_ops_gpu import BF16, DEV, F32, close, gen, ints, make_cache, q4_weight, randn
+
+pytestmark = pytest.mark.gpu
+U = ref.U
+
+
+def exact_gradient(logits, tokens, temperature, gl, ge):
+    raw, given = logits.cpu().double(), tokens.cpu().long()
+    vocab, t = raw.shape[1], float(torch.tensor(temperature))
+    top = raw.amax(-1, keepdim=True)
+    d = torch.where(raw == -math.inf, -math.inf, (raw - torch.nan_to_num(top, neginf=0.0)) / t)
+    lse0 = d.logsumexp(-1, keepdim=True)
+    logp = torch.where(raw == -math.inf, -math.inf, d - lse0)
+    p = logp.exp()
+    safe = torch.where(p > 0, logp, 0.0)
+    h = torch.special.entr(p).sum(-1, keepdim=True)
+    has = ((given >= 0) & (given < vocab)).double()[:, None]
+    hot = torch.zeros_like(p).scatter_(1, given.clamp(0, vocab - 1)[:, None], has)
+    gl = torch.zeros_like(has) if gl is None else gl.cpu().double()[:, None] * has
+    ge = torch.zeros_like(has) if ge is None else ge.cpu().double()[:, None]
+    live = (raw > -math.inf).double()
+    grad = (gl * (hot - p) - ge * p * (safe + h)) / t * live
+    lse = (top / t + lse0).abs()
+    off = 2.0 ** -24 * torch.where(lse < 1024, lse, 0.0) + 2.0 ** -22 * (16 + safe.abs().clamp(max=200))
+    size = (gl.abs() * (hot * live + p) + ge.abs() * p * (safe.abs() + h + 1)) / t
+    return grad, (off + 8 * U + vocab / 256 * 2.0 ** -24) * size
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 8.0])
+@pytest.mark.parametrize("vocab", [37, 5003, 40000])
+def test_gradient_of_rows_of_large_magnitude(dtype, temperature, vocab):
+    """Rows where the fp32 lse leaves no room for ln V, and the type's lowest value as a mask, of some tokens or all."""
+    g = gen(vocab)
+    lowest = torch.finfo(dtype).min * 0.5 if temperature < 1 else torch.finfo(dtype).min
+    logits = randn(g, 12, vocab).to(dtype)
+    logits[0] = lowest
+    logits[1] = lowest
+    logits[1, vocab // 2] = 3.0
+    logits[2] = -1e9
+    logits[3] = 1e9
+    logits[4] -= 2000
+    logits[5] = logits[5] * 4 + 30000
+    logits[6] = logits[6] * 1e6
+    logits[7] = -1e9
+    logits[7, ::3] = -math.inf
+    logits[8] = -1e30
+    logits[8, 5:11] = randn(g, 6).to(dtype)
+    logits[9] += 700
+    logits[10] = lowest
+    logits[10, 1::2] = -math.inf
+    tokens = torch.randint(vocab, (12,), device=DEV, generator=g).to(torch.int32)
+    for given in (tokens, torch.full_like(tokens, -1)):
+        fw = mtp.mtp_token_logprobs(logits, given, temperature=temperature)
+        for gl, ge in ((randn(g, 12), randn(g, 12)), (randn(g, 12), None), (None, randn(g, 12))):
+            got = mtp.mtp_token_logprobs_backward(logits, given, fw.lse, fw.entropy, gl, ge, temperature)
+            want, tol = exact_gradient(logits, given, temperature, gl, ge)
+            close(got, want, tol + (2.0 ** -8 * want.abs() if dtype == BF16 else 0.0) + 1e-37, f"{gl is None} {ge is None}")
+
+
+def test_gradient_of_masked_tokens_with_large_weights():
+    """A token without weight gets 0, not 0 times an overflow, however large the entropy's weight is."""
+    g = gen(41)
+    logits = randn(g, 4, 1000)
+    logits[:, ::2] = -math.inf
+    tokens = ints([1, 3, 5, 7])
+    fw = mtp.mtp_token_logprobs(logits, tokens, temperature=1e-3)
+    ge = torch.full((4,), 1e7, device=DEV)
+    got = mtp.mtp_token_logprobs_backward(logits, tokens, fw.lse, fw.entropy, ge, ge, 1e-3)
+    assert torch.isfinite(got).all() and (got[:, ::2] == 0).all()
