@@ -2,7 +2,8 @@
 
 Thin Python face of the C ABI in include/mtp_lm_ops.h, in the manner of the package's head: each ``mtp_``
 function has the name of the C entry point that it calls, takes torch tensors, runs on the current stream (or
-``stream``), allocates the outputs that the caller did not pass, and raises ``MtpError`` on a non-OK status.
+``stream``), allocates the outputs that the caller did not pass, and raises ``MtpError`` on a non-OK status.  A call
+with a ``stream`` is the call under ``torch.cuda.stream(stream)``: what it allocates belongs to that stream.
 
     weight = Q4Weight.quantize(w, group=64)                    # once
     logits = mtp_q4_matvec(weight, hidden)                     # [B, M] fp32
@@ -73,6 +74,12 @@ class Q4Weight:
     """
 
     def __init__(self, codes, scales, zeros=None, stream=None):
+        if stream is not None:
+            for t in (codes, scales, zeros):
+                if t is not None:
+                    t.record_stream(stream)   # the caller may drop them before it has packed them
+            with torch.cuda.stream(stream):
+                return Q4Weight.__init__(self, codes, scales, zeros)
         assert codes.dtype == torch.uint8 and codes.dim() == 2 and codes.stride(1) == 1
         assert scales.dtype == torch.bfloat16 and scales.is_contiguous() and scales.device == codes.device
         assert scales.dim() == 2 and scales.shape[0] == codes.shape[0]
@@ -87,17 +94,23 @@ class Q4Weight:
         self.desc = MtpQ4Desc(rows=self.rows, cols=self.cols, group=self.group, zeros=zeros is not None,
                               device=self.index, packed=self.packed.data_ptr(), softcap=0.0)
         check(lib().mtp_q4_pack(ctypes.byref(self.desc), codes.data_ptr(), codes.stride(0) if self.rows > 1 else self.cols // 2,
-                                scales.data_ptr(), _ptr(zeros), self.packed.data_ptr(), size, _stream(stream, self.index)),
+                                scales.data_ptr(), _ptr(zeros), self.packed.data_ptr(), size, _raw_stream(self.index)),
               "mtp_q4_pack")
 
     @classmethod
     def quantize(cls, w, group=64, zeros=False, stream=None):
         """The 4-bit form of a bf16 matrix (mtp_q4_quantize), a one-time step."""
-        return cls(*mtp_q4_quantize(w, group, zeros, stream), stream=stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return cls.quantize(w, group, zeros)
+        return cls(*mtp_q4_quantize(w, group, zeros))
 
 
 def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
     """(codes, scales, zeros or None) of the bf16 matrix w [M, K] (unit inner stride, finite values)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mtp_q4_quantize(w, group, zeros)
     assert w.dtype == torch.bfloat16 and w.dim() == 2 and w.stride(1) == 1
     rows, cols = w.shape
     codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
@@ -105,12 +118,15 @@ def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
     points = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zeros else None
     check(lib().mtp_q4_quantize(w.data_ptr(), w.stride(0) if rows > 1 else cols, rows, cols, group, w.device.index or 0,
                                 codes.data_ptr(), max(1, cols // 2), scales.data_ptr(), _ptr(points),
-                                _stream(stream, w.device.index or 0)), "mtp_q4_quantize")
+                                _raw_stream(w.device.index or 0)), "mtp_q4_quantize")
     return codes, scales, points
 
 
 def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, stream=None):
     """[B, M]: softcap(x @ w.T) of x bf16 [B, K], in fp32 or rounded once to bf16 (out's type, or out_dtype)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mtp_q4_matvec(weight, x, out, out_dtype, softcap)
     batch, cols = x.shape
     rows, where = weight.rows, weight.where
     x_strides = x.stride()
@@ -125,7 +141,7 @@ def mtp_q4_matvec(weight, x, out=None, out_dtype=torch.float32, softcap=0.0, str
         desc.softcap = softcap
     many = batch > 1
     check(lib().mtp_q4_matvec(desc, x.data_ptr(), x_strides[0] if many else cols, batch, out.data_ptr(), _TYPES[out.dtype],
-                              out_strides[0] if many else rows, _stream(stream, weight.index)), "mtp_q4_matvec")
+                              out_strides[0] if many else rows, _raw_stream(weight.index)), "mtp_q4_matvec")
     return out
 
 
@@ -232,6 +248,9 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
     lengths are the tokens of each sequence in the cache, with the ones that q belongs to; starts and max_q as
     in mtp_kv_append; max_len bounds the lengths (0: the table's width); window 0 sees everything; scale is
     head_dim ** -0.5 unless given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mtp_kv_attention(cache, page_table, lengths, q, starts, max_q, max_len, window, scale, out, lse, workspace)
     shape, where = q.shape, cache.where
     tokens, heads, dim = shape
     strides = q.stride()
@@ -251,11 +270,11 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
             if len(cache._needs) > 4096:
                 cache._needs.clear()
             need = cache._needs[key] = library.mtp_kv_attention_workspace_bytes(desc, seqs, heads, max_len, window)
-        workspace = cache.workspace(need, stream)
+        workspace = cache.workspace(need)
     check(library.mtp_kv_attention(desc, seqs, q.data_ptr(), strides[0], strides[1], heads, max_len, window,
                                    dim ** -0.5 if scale is None else scale, _vector(out, torch.bfloat16, tokens * heads * dim, where),
                                    _vector(lse, torch.float32, tokens * heads, where), workspace.data_ptr(),
-                                   workspace.numel(), _stream(stream, cache.index)), "mtp_kv_attention")
+                                   workspace.numel(), _raw_stream(cache.index)), "mtp_kv_attention")
     return out, lse
 
 
@@ -284,6 +303,9 @@ def _rows(t):
 def mtp_token_logprobs(logits, tokens, top=0, temperature=1.0, out=None, stream=None) -> TokenLogprobs:
     """Log probability and rank of tokens[r] (int32 [rows]; outside the vocabulary: no token) in logits[r], the
     row's entropy and lse, and its `top` largest alternatives.  out: an earlier result to write into."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mtp_token_logprobs(logits, tokens, top, temperature, out)
     rows, vocab, ld = _rows(logits)
     where, kind = logits.get_device(), _TYPES[logits.dtype]
     f32, i32 = torch.float32, torch.int32
@@ -298,7 +320,7 @@ def mtp_token_logprobs(logits, tokens, top=0, temperature=1.0, out=None, stream=
                                    _vector(logprob, f32, rows, where), _vector(entropy, f32, rows, where),
                                    _vector(rank, i32, rows, where), _vector(lse, f32, rows, where),
                                    _vector(top_ids, i32, rows * top, where), _vector(top_logprobs, f32, rows * top, where),
-                                   where, _stream(stream, where)), "mtp_token_logprobs")
+                                   where, _raw_stream(where)), "mtp_token_logprobs")
     return out
 
 
@@ -306,6 +328,9 @@ def mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad
                                 stream=None):
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with respect to the logits, in their
     type.  out may be the logits themselves."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, temperature, out)
     rows, vocab, ld = _rows(logits)
     where, dtype, f32 = logits.get_device(), logits.dtype, torch.float32
     if out is None:
@@ -315,7 +340,7 @@ def mtp_token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad
     check(lib().mtp_token_logprobs_backward(
         logits.data_ptr(), _TYPES[dtype], ld, rows, vocab, _vector(tokens, torch.int32, rows, where), temperature,
         _vector(lse, f32, rows, where), _vector(entropy, f32, rows, where), _vector(grad_logprob, f32, rows, where),
-        _vector(grad_entropy, f32, rows, where), out.data_ptr(), ld_out, where, _stream(stream, where)),
+        _vector(grad_entropy, f32, rows, where), out.data_ptr(), ld_out, where, _raw_stream(where)),
         "mtp_token_logprobs_backward")
     return out
 

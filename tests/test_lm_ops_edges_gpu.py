@@ -78,3 +78,40 @@ def test_gradient_of_masked_tokens_with_large_weights():
     ge = torch.full((4,), 1e7, device=DEV)
     got = mtp.mtp_token_logprobs_backward(logits, tokens, fw.lse, fw.entropy, ge, ge, 1e-3)
     assert torch.isfinite(got).all() and (got[:, ::2] == 0).all()
+
+
+def test_calls_on_a_delayed_side_stream():
+    """Calls with `stream`, late behind other work, while the current stream allocates and fills blocks of the sizes
+    that they took: the same results as on the current stream."""
+    g = gen(42)
+    w = (randn(g, 640, 2048) * 0.02).to(BF16)
+    x, logits = randn(g, 6, 2048).to(BF16), randn(g, 12, 5003)
+    tokens, weights = torch.arange(12, dtype=torch.int32, device=DEV), randn(g, 12)
+    cache, table = make_cache(g, [900, 60, 300], 2, 128, 32, "int8")
+    lengths, q = ints([900, 60, 300]), randn(g, 3, 8, 128).to(BF16)
+
+    def calls(**s):
+        parts = mtp.mtp_q4_quantize(w, 32, True, **s)
+        weight = mtp.Q4Weight(*parts, **s)
+        del parts
+        product = mtp.mtp_q4_matvec(mtp.Q4Weight.quantize(w, 64, **s), x, **s)
+        scored = mtp.mtp_token_logprobs(logits, tokens, top=4, **s)
+        grad = mtp.mtp_token_logprobs_backward(logits, tokens, scored.lse, scored.entropy, weights, **s)
+        out, _ = mtp.mtp_kv_attention(cache, table, lengths, q, **s)
+        return [weight.packed, product, out, grad, *scored]
+
+    def sizes(t):
+        return t.numel() * t.element_size()
+
+    want = calls()
+    taken = {640 * 1024, 640 * 64 * 2, 640 * 64, 640 * 32 * 2, 3 * 8 * 4, *map(sizes, want)}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = calls(stream=side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in taken for _ in range(6)]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all((t == 255).all() for t in junk)
