@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
             const int r = m * 8 + 2 * t + e;
             factor[m][e] = s_factor[r] * UNIT;
             bias[m][e] = INT8 ? s_bias[r] : 0.f;
-            here[m][e] = (int)min(base + (r0 + min(r, live - 1)) / share, (long long)cap);
+            // the window counts from the position even where that is beyond the table; before 0 is before 0
+            here[m][e] = (int)max(base + (r0 + min(r, live - 1)) / share, -1ll);
             top[m][e] = -INFINITY;
             l_round[m][e] = l_sum[m][e] = 0.f;
         }

@@ -115,3 +115,48 @@ def test_calls_on_a_delayed_side_stream():
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all((t == 255).all() for t in junk)
+
+
+def one_row(q, k, v, scale):
+    q, k, v = q.cpu().double(), k.cpu().double(), v.cpu().double()
+    if not k.shape[0]:
+        z = torch.zeros_like(q)
+        return z, z, torch.tensor(-math.inf).double(), torch.tensor(0.0)
+    s = scale * (k @ q)
+    ds = (q.shape[0] + 8) * U * abs(scale) * (k.abs() @ q.abs()).max() + 2.0 ** -21 * (1 + s.abs().max())
+    p, chain = s.softmax(0), (64 + k.shape[0] / 16) * U
+    o, size = p @ v, p @ v.abs()
+    # weights have 11 bits, or 2^-32 of the largest
+    tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * ds + 2 * chain) * size + k.shape[0] * 2.0 ** -32 * v.abs().amax(0) * p.max()
+    lse = s.logsumexp(0)
+    return o, tol, lse, ds + chain + 4 * U * lse.abs()
+
+
+def tokens_of(cache, table_row, length, head):
+    pages = table_row[:-(-length // cache.page_tokens)].long()
+    out = []
+    for codes, scales in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        x = ref.decode(codes[pages][:, head], cache.format) * scales[pages][:, head].cpu().double()[:, None, None]
+        out.append(x.flatten(0, 1)[:length])
+    return out
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("count", [1, 3])
+@pytest.mark.parametrize("over,window", [(100, 200), (1, 7), (60, 70), (500, 40), (37, 0)])
+def test_attention_longer_than_its_table_with_a_window(fmt, count, over, window):
+    """What lies behind the table is left out, and nothing else: the window still counts from the true position."""
+    g = gen(over)
+    cap = 320
+    cache, table = make_cache(g, [cap], 2, 64, 16, fmt)
+    q = randn(g, count, 4, 64).to(BF16)
+    out, lse = mtp.mtp_kv_attention(cache, table, ints([cap + over]), q, window=window)
+    assert cache.read_errors() == mtp.MTP_DEVERR_PAGE
+    for i in range(count):
+        p = cap + over - count + i
+        low = max(0, p - window + 1) if window else 0
+        for h in range(4):
+            k, v = tokens_of(cache, table[0], cap, h // 2)
+            o, tol, l, ltol = one_row(q[i, h], k[low:p + 1], v[low:p + 1], 0.125)
+            close(out[i, h], o, tol)
+            close(lse[i, h], l, ltol)
