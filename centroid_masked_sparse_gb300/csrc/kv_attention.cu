@@ -103,13 +103,13 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
     wait_for_previous();
     const long long length = __ldg(c.lengths + b);
     int row0, n;
-    kv_rows(c, b, &row0, &n);
+    const int brought = kv_rows(c, b, &row0, &n);
     const int r0 = (blockIdx.y - h * p.row_tiles) * R, live = min(R, n * share - r0);
     if (live <= 0) return;
     const int cap = c.table_width * c.page_tokens;
     if ((length < 0 || length > cap) && c.err && threadIdx.x == 0) atomicOr(c.err, MTP_DEVERR_PAGE);
     // query i stands at position base + i; positions [lo, end) are seen by some row
-    const long long base = length - n;
+    const long long base = length - brought;
     const int q_lo = r0 / share, q_hi = (r0 + live - 1) / share;
     const int lo = p.window > 0 ? (int)max(0ll, base + q_lo - p.window + 1) : 0;
     const int end = (int)max(0ll, min(base + q_hi + 1, (long long)cap));

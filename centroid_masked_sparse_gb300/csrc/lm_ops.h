@@ -140,21 +140,21 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, int
 // ---------------------------------------------------------------------------
 
 // The rows of a call that sequence b brings, clipped to [0, tokens) and max_tokens; what
-// is clipped sets MTP_DEVERR_OFFSETS.
-__device__ __forceinline__ void kv_rows(const KvParams &c, int b, int *first, int *count)
+// is clipped sets MTP_DEVERR_OFFSETS.  Returns how many it brings with those beyond max_tokens.
+__device__ __forceinline__ int kv_rows(const KvParams &c, int b, int *first, int *count)
 {
     if (c.starts == nullptr) {
         *count = c.tokens / c.batch;
         *first = b * *count;
-        return;
+        return *count;
     }
     const int lo = __ldg(c.starts + b), hi = __ldg(c.starts + b + 1);
-    int n = hi - lo;
-    if (lo < 0 || hi < lo || hi > c.tokens) n = 0;
-    if (n > c.max_tokens) n = c.max_tokens;
-    if (n != hi - lo && c.err) atomicOr(c.err, MTP_DEVERR_OFFSETS);
+    const bool good = lo >= 0 && hi >= lo && hi <= c.tokens;
+    const int all = good ? hi - lo : 0;
     *first = lo;
-    *count = n;
+    *count = min(all, c.max_tokens);
+    if ((!good || *count != all) && c.err) atomicOr(c.err, MTP_DEVERR_OFFSETS);
+    return all;
 }
 
 __device__ __forceinline__ float bf16_value(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }

@@ -111,7 +111,7 @@ MTP_API mtp_status mtp_q4_quantize(const void *w, int64_t ld_w, int32_t rows, in
  *                       its tokens are skipped (not written, not attended to)
  *   MTP_DEVERR_OFFSETS  starts not ascending inside [0, tokens], or more tokens in a
  *                       sequence than max_tokens: the tokens beyond are skipped (their
- *                       outputs are not written) */
+ *                       outputs are not written), the others keep their places */
 #define MTP_DEVERR_PAGE 0x8u
 
 /* A paged cache of keys and values.  A page holds page_tokens consecutive tokens of one

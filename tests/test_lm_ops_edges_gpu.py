@@ -160,3 +160,27 @@ def test_attention_longer_than_its_table_with_a_window(fmt, count, over, window)
             o, tol, l, ltol = one_row(q[i, h], k[low:p + 1], v[low:p + 1], 0.125)
             close(out[i, h], o, tol)
             close(lse[i, h], l, ltol)
+
+
+@pytest.mark.parametrize("window", [0, 9])
+def test_attention_keeps_the_places_of_tokens_within_the_bound(window):
+    g = gen(31)
+    lengths, counts = [50, 37], [6, 4]
+    cache, table = make_cache(g, lengths, 1, 64, 16, "int8")
+    q = randn(g, 10, 2, 64).to(BF16)
+    full = mtp.mtp_kv_attention(cache, table, ints(lengths), q, starts=ints([0, 6, 10]), max_q=6, window=window)
+    out, lse = torch.full_like(full[0], 9.0), torch.full_like(full[1], 9.0)
+    mtp.mtp_kv_attention(cache, table, ints(lengths), q, starts=ints([0, 6, 10]), max_q=4, window=window, out=out, lse=lse)
+    assert cache.read_errors() == mtp.MTP_DEVERR_OFFSETS
+    for row in range(10):
+        if row in (4, 5):
+            assert (out[row] == 9).all() and (lse[row] == 9).all()
+        else:
+            for h in range(2):
+                b, i = (0, row) if row < 6 else (1, row - 6)
+                p = lengths[b] - counts[b] + i
+                low = max(0, p - window + 1) if window else 0
+                k, v = tokens_of(cache, table[b], lengths[b], 0)
+                o, tol, l, ltol = one_row(q[row, h], k[low:p + 1], v[low:p + 1], 0.125)
+                close(out[row, h], o, tol)
+                close(lse[row, h], l, ltol)
