@@ -1,5 +1,6 @@
 // C ABI of the operators around the head: argument checks and launches.  Declarations and
 // the contract of every entry point are in include/mtp_lm_ops.h.
+#include <algorithm>
 #include <cmath>
 
 #include "lm_ops.h"
@@ -70,7 +71,7 @@ KvParams kv_params(const mtp_kv_desc *d, const mtp_kv_batch *s)
     c.starts = s->starts;
     c.batch = s->batch;
     c.tokens = s->tokens;
-    c.max_tokens = s->max_tokens;
+    c.max_tokens = std::min(s->max_tokens, s->tokens);   // a bound of any size costs what the call's tokens do
     return c;
 }
 
@@ -211,7 +212,8 @@ mtp_status mtp_kv_attention(const mtp_kv_desc *d, const mtp_kv_batch *seqs, cons
     if (heads < 1 || heads % d->kv_heads != 0 || max_len < 0 || window < 0) return MTP_ERR_SHAPE;
     if (heads > 65535) return MTP_ERR_UNSUPPORTED;
     if (seqs->batch == 0 || seqs->tokens == 0) return MTP_OK;
-    if ((int64_t)(seqs->starts ? seqs->max_tokens : seqs->tokens / seqs->batch) * heads > 1 << 19) return MTP_ERR_UNSUPPORTED;
+    if ((int64_t)(seqs->starts ? std::min(seqs->max_tokens, seqs->tokens) : seqs->tokens / seqs->batch) * heads > 1 << 19)
+        return MTP_ERR_UNSUPPORTED;
     if ((st = check_strides(q, q_token_stride, q_head_stride)) != MTP_OK) return st;
     if (!out) return MTP_ERR_NULL;
     if (!workspace || workspace_bytes < MTP_KV_WORKSPACE_ZEROED) return MTP_ERR_WORKSPACE;

@@ -144,7 +144,8 @@ typedef struct mtp_kv_desc {
 /* The sequences of a call and the tokens that each brings.
  *   batch        sequences, 0..65535
  *   tokens       tokens of the call in all (rows of k, v or q)
- *   max_tokens   the most tokens that one sequence brings (a bound, >= 1)
+ *   max_tokens   the most tokens that one sequence brings (a bound, >= 1; above `tokens` it
+ *                counts as `tokens`)
  *   table_width  page ids per sequence in the table, >= 1, table_width * page_tokens <= 2^30
  *   page_table   int32 [batch, ld_table]: page of a sequence's tokens
  *                [i * page_tokens, (i + 1) * page_tokens) at column i; columns that no
@@ -186,7 +187,7 @@ MTP_API mtp_status mtp_kv_append(const mtp_kv_desc *desc, const mtp_kv_batch *se
  *   o = sum_j e^(s_j - lse) v_j,   s_j = scale * (q . k_j),   lse = ln sum_j e^(s_j)
  * A query that sees nothing (p < 0) gets o = 0 and lse = -inf.
  *   q        bf16 [tokens, heads, head_dim], strides as for mtp_kv_append
- *   heads    a multiple of kv_heads, max_tokens * heads <= 2^19
+ *   heads    a multiple of kv_heads, max_tokens * heads <= 2^19 (without starts: tokens / batch * heads)
  *   max_len  a bound on the lengths that decides how the work is split (any length is
  *            right); 0: table_width * page_tokens
  *   out      bf16 [tokens, heads, head_dim] contiguous, 16-byte aligned

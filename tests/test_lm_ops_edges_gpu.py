@@ -184,3 +184,25 @@ def test_attention_keeps_the_places_of_tokens_within_the_bound(window):
                 o, tol, l, ltol = one_row(q[row, h], k[low:p + 1], v[low:p + 1], 0.125)
                 close(out[row, h], o, tol)
                 close(lse[row, h], l, ltol)
+
+
+def test_attention_bound_far_above_the_tokens():
+    g = gen(34)
+    cache, table = make_cache(g, [50, 37], 2, 64, 16, "int8")
+    q = randn(g, 5, 4, 64).to(BF16)
+    want = mtp.mtp_kv_attention(cache, table, ints([50, 37]), q, starts=ints([0, 2, 5]), max_q=5)
+    got = mtp.mtp_kv_attention(cache, table, ints([50, 37]), q, starts=ints([0, 2, 5]), max_q=2 ** 31 - 1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_append_bound_far_above_the_tokens():
+    g = gen(39)
+    k, v = (randn(g, 40, 2, 64).to(BF16) for _ in range(2))
+    caches = []
+    for most in (37, 2 ** 31 - 1):
+        cache = mtp.KvCache.allocate(6, 16, 2, 64, "e4m3")
+        mtp.mtp_kv_append(cache, ints([[0, 1, 2], [3, 4, 5]]), ints([0, 7]), k, v, starts=ints([0, 37, 40]), max_new=most)
+        assert cache.read_errors() == 0
+        caches.append(cache)
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        assert torch.equal(*(getattr(c, name) for c in caches))

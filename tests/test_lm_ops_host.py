@@ -172,3 +172,15 @@ def test_token_logprobs_backward_refuses(L, kw, expect):
                 gl=0x4200, ge=None, grad=0x5000, ld_grad=1000), **kw}
     assert L.mtp_token_logprobs_backward(c["logits"], c["type"], c["ld"], c["rows"], c["vocab"], c["tokens"], c["temperature"], c["lse"],
                                          c["entropy"], c["gl"], c["ge"], c["grad"], c["ld_grad"], 0, None) == expect
+
+
+def test_kv_bound_above_the_tokens_counts_as_the_tokens(L):
+    """A capacity as the most tokens of a sequence neither makes a call too large nor its workspace larger."""
+    ragged = dict(batch=2, tokens=5, starts=0x70000, table_width=4096, ld_table=4096)
+    need = [L.mtp_kv_attention_workspace_bytes(ctypes.byref(kv()), ctypes.byref(seqs(max_tokens=n, **ragged)), 8, 0, 0)
+            for n in (5, 100, 1 << 20, (1 << 31) - 1)]
+    assert len(set(need)) == 1
+    for n in (5, 1 << 20, (1 << 31) - 1):
+        # short of the workspace, which is looked at after the sizes
+        assert L.mtp_kv_attention(ctypes.byref(kv()), ctypes.byref(seqs(max_tokens=n, **ragged)), 0x80000, 1024, 128, 8, 0, 0, 0.1,
+                                  0x90000, None, 0xb0000, 1000, None) == WORKSPACE
