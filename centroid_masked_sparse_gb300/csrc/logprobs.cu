@@ -6,8 +6,8 @@
 // logits x, where R is the integer above its largest x c: then x c - R is one fused
 // multiply-add with one rounding, R is exact and so are the powers of two that join the
 // threads' sums; ln sum e^x = (R + log2 s) ln 2, entropy = (log2 s - t / s) ln 2.  A row
-// whose largest |x c| is 2^22 or more (all logits at the type's lowest value, say) is read
-// again with its maximum m and terms of (x - m) c.
+// whose largest |x c| is 2^22 or more (all logits at the type's lowest value, say), or a
+// temperature of 2^64 or more, is read again with its maximum m and terms of (x - m) c.
 //
 // The alternatives: each of the W warps finds the ceil(n / W)-th largest of its threads'
 // largest logits; the lowest of these is a bound that at least n logits reach, and few do.
@@ -34,6 +34,7 @@ constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;          // 16-byte vectors of a thread in a tile
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kFar = 4194304.f; // |x c| from which R would not be exact
+constexpr float kFlat = 0x1p-64f; // 1 / temperature below which `low` (see there) would have a weight
 
 typedef unsigned long long u64;
 
@@ -117,7 +118,8 @@ template <bool BF16> __device__ __forceinline__ float element(const uint4 &v, in
     return BF16 ? (e % 2 ? bf_hi(w) : bf_lo(w)) : __uint_as_float(w);
 }
 
-// What stands in for lower logits: their terms are 0 all the same, and it keeps 0 * -inf out.
+// What stands in for lower logits: their terms are 0 all the same (for factors from kFlat on,
+// below which a second reading takes the terms), and it keeps 0 * -inf out.
 __device__ __forceinline__ float lowest(float factor) { return -1e30f / fmaxf(factor, 1.f); }
 
 // The warp's 32 keys in falling order, and the largest 32 of two such lists.
@@ -524,13 +526,14 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     };
     const float2 s1 = unpair(s2), t1 = unpair(t2);
     Sums sums = join_all(Sums{r, s1.x + s1.y, t1.x + t1.y, most, before}, true);
-    const bool far = fabsf(sums.most * c) >= kFar && fabsf(sums.most) < INFINITY;
+    const bool flat = p.factor < kFlat, far = sums.most < INFINITY && (flat || (sums.most > -INFINITY && fabsf(sums.most * c) >= kFar));
+    auto below = [&](float v, float m) { return v * 0.5f - m * 0.5f; };   // half of v - m, which may leave fp32's range
     if (far) {
-        // once more, with the maximum
-        const float m = sums.most;
+        // once more, with the maximum (any finite number where all is masked)
+        const float m = fmaxf(sums.most, -3.402823466e38f);
         float s = 0.f, t = 0.f;
         auto term = [&](float v) {
-            const float d = max_nan((v - m) * c, -200.f), e = exp2_fast(d);
+            const float d = max_nan(below(v, m) * (2.f * c), -200.f), e = exp2_fast(d);
             s += e, t = fmaf(e, d, t);
         };
         if (crank == 0 && threadIdx.x < head) term(L::value(x[threadIdx.x]));
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         const float ln_s = logf(s), log2_s = log2f(s);
         auto logprob = [&](float v) {
             if (v == -INFINITY) return -INFINITY + s * 0.f;
-            if (far) return fmaf(v - sums.most, p.factor, -ln_s);
+            if (far) return fmaf(below(v, sums.most), 2.f * p.factor, -ln_s);
             if (v * c < -kFar) return fmaf(v, p.factor, -(sums.r + log2_s) * kLn2);   // v c may leave fp32's range
             return (fmaf(v, c, -sums.r) - log2_s) * kLn2;
         };

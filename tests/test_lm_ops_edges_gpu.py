@@ -206,3 +206,37 @@ def test_append_bound_far_above_the_tokens():
         caches.append(cache)
     for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
         assert torch.equal(*(getattr(c, name) for c in caches))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("temperature", [1e20, 1e24, 2.0 ** 90, 1e28, 1e30, 1e33, 1e37])
+def test_logprobs_at_very_high_temperatures(dtype, temperature):
+    """Masked tokens have no probability where 1e30 / temperature is small, and logits at both ends of the type have one."""
+    g = gen(37)
+    for vocab in (50, 9000):
+        logits = (randn(g, 7, vocab) * 3).to(dtype)
+        logits[1, ::2] = -math.inf
+        logits[2] = (randn(g, vocab) * 1e30).to(dtype)
+        logits[2, 1::3] = -math.inf
+        logits[3] = -math.inf
+        logits[3, 4] = 1.0
+        logits[4] = -math.inf
+        logits[5] = torch.finfo(dtype).min
+        logits[5, ::2] = torch.finfo(dtype).max
+        logits[5, ::3] = -math.inf
+        logits[6, 7] = math.nan
+        tokens = ints([1, 2, 1, 4, 5, 7, 3])
+        got = mtp.mtp_token_logprobs(logits, tokens, top=5, temperature=temperature)
+        want = ref.logprobs(logits, tokens, temperature, 5)
+        for name, (value, tol) in want.items():
+            mine = getattr(got, name)
+            if tol is None:
+                assert torch.equal(mine[:6].cpu().long(), value[:6].long()), name
+            else:
+                close(mine[:6], value[:6], tol[:6], name)
+                assert torch.isnan(mine[6]).all()
+        gl, ge = randn(g, 7), randn(g, 7)
+        grad = mtp.mtp_token_logprobs_backward(logits, tokens, got.lse, got.entropy, gl, ge, temperature)
+        want, tol = exact_gradient(logits[:6], tokens[:6], temperature, gl[:6], ge[:6])
+        # bf16: 2^-9 of a value (allowed: twice that), or half of the smallest subnormal
+        close(grad[:6], want, tol + (2.0 ** -8 * want.abs() + 2.0 ** -134 if dtype == BF16 else 0.0) + 1e-44)
