@@ -119,8 +119,12 @@ template <bool BF16> __device__ __forceinline__ float element(const uint4 &v, in
 }
 
 // What stands in for lower logits: their terms are 0 all the same (for factors from kFlat on,
-// below which a second reading takes the terms), and it keeps 0 * -inf out.
-__device__ __forceinline__ float lowest(float factor) { return -1e30f / fmaxf(factor, 1.f); }
+// below which a second reading takes the terms), and it keeps 0 * -inf out.  A bf16 number, so
+// that no logit of that type lies between it and what it is rounded to.
+__device__ __forceinline__ float lowest(float factor)
+{
+    return __uint_as_float(__float_as_uint(-1e30f / fmaxf(factor, 1.f)) & 0xffff0000u);
+}
 
 // The warp's 32 keys in falling order, and the largest 32 of two such lists.
 template <typename K> __device__ __forceinline__ K exchange(K v, int lane, int step, bool up)
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
     const T *x = (const T *)p.logits + row * p.ld;
     const float c = p.factor * kLog2e;
     const float low = lowest(p.factor);
-    const uint32_t low2 = bf16_bits(low) * 0x10001u;
+    const uint32_t low2 = (__float_as_uint(low) >> 16) * 0x10001u;
 
     // The row as scalars up to a 16-byte boundary, vectors, and scalars behind the last; the
     // first CTA takes the scalars before, the last one those behind, and each its vectors.

@@ -240,3 +240,18 @@ def test_logprobs_at_very_high_temperatures(dtype, temperature):
         want, tol = exact_gradient(logits[:6], tokens[:6], temperature, gl[:6], ge[:6])
         # bf16: 2^-9 of a value (allowed: twice that), or half of the smallest subnormal
         close(grad[:6], want, tol + (2.0 ** -8 * want.abs() + 2.0 ** -134 if dtype == BF16 else 0.0) + 1e-44)
+
+
+@pytest.mark.parametrize("temperature", [0.7, 0.3, 0.6, 1.0])
+def test_rank_at_the_replacement_of_masked_logits(temperature):
+    """A given logit near the number that stands in for -inf inside: the masked tokens do not come before it."""
+    factor = torch.tensor(1.0 / temperature, dtype=F32)
+    value = (torch.tensor(-1e30) / factor.clamp(min=1)).to(BF16)
+    near = (value.view(torch.int16) + torch.tensor([-2, -1, 0, 1, 2], dtype=torch.int16)).view(BF16)
+    for at in near:
+        logits = torch.full((1, 20000), -math.inf, dtype=BF16, device=DEV)
+        logits[0, 15000] = at
+        logits[0, 3:9] = 1.0
+        logits[0, 12000] = value.item() * 2
+        got = mtp.mtp_token_logprobs(logits, ints([15000]), temperature=temperature)
+        assert got.rank.item() == 6
