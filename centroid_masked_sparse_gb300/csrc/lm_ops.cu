@@ -80,7 +80,8 @@ mtp_status check_logits(int32_t type, int64_t ld, int32_t rows, int32_t vocab, f
 {
     if (type != MTP_TYPE_F32 && type != MTP_TYPE_BF16) return MTP_ERR_UNSUPPORTED;
     if (rows < 0 || vocab < 1 || ld < vocab || device < 0) return MTP_ERR_SHAPE;
-    if (!(temperature > 0.f) || std::isinf(temperature) || std::isinf((float)(1.0 / temperature))) return MTP_ERR_SHAPE;
+    // the kernels multiply by log2(e) / temperature
+    if (!(temperature > 0.f) || std::isinf(temperature) || std::isinf((float)(1.4426950408889634 / temperature))) return MTP_ERR_SHAPE;
     return MTP_OK;
 }
 

@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         const float m = fmaxf(sums.most, -3.402823466e38f);
         float s = 0.f, t = 0.f;
         auto term = [&](float v) {
-            const float d = max_nan(below(v, m) * (2.f * c), -200.f), e = exp2_fast(d);
+            const float d = max_nan(below(v, m) * c * 2.f, -200.f), e = exp2_fast(d);
             s += e, t = fmaf(e, d, t);
         };
         if (crank == 0 && threadIdx.x < head) term(L::value(x[threadIdx.x]));
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
         const float ln_s = logf(s), log2_s = log2f(s);
         auto logprob = [&](float v) {
             if (v == -INFINITY) return -INFINITY + s * 0.f;
-            if (far) return fmaf(below(v, sums.most), 2.f * p.factor, -ln_s);
+            if (far) return fmaf(below(v, sums.most) * p.factor, 2.f, -ln_s);
             if (v * c < -kFar) return fmaf(v, p.factor, -(sums.r + log2_s) * kLn2);   // v c may leave fp32's range
             return (fmaf(v, c, -sums.r) - log2_s) * kLn2;
         };

@@ -227,7 +227,7 @@ MTP_API mtp_status mtp_kv_attention(const mtp_kv_desc *desc, const mtp_kv_batch 
  *   logits       [rows, ld] of type (MTP_TYPE_*), aligned to its element, ld >= vocab
  *   tokens       int32 [rows], an id outside [0, vocab) marking a row without one; NULL
  *                if logprob and rank are NULL
- *   temperature  > 0 and finite, as its reciprocal
+ *   temperature  > 0 and finite, as log2(e) / temperature (4.3e-39 and up)
  *   top          0..MTP_MAX_TOP alternatives (top_ids and top_logprobs [rows, top])
  * Every output may be NULL; NULL top_ids with top > 0 gives MTP_ERR_NULL. */
 MTP_API mtp_status mtp_token_logprobs(const void *logits, int32_t type, int64_t ld, int32_t rows, int32_t vocab,

@@ -255,3 +255,16 @@ def test_rank_at_the_replacement_of_masked_logits(temperature):
         logits[0, 12000] = value.item() * 2
         got = mtp.mtp_token_logprobs(logits, ints([15000]), temperature=temperature)
         assert got.rank.item() == 6
+
+
+@pytest.mark.parametrize("temperature", [4.4e-39, 6e-39, 1e-38])
+def test_logprobs_at_the_lowest_temperatures(temperature):
+    """One over the temperature is near fp32's end: the largest logit has all of the probability."""
+    logits = torch.zeros(3, 5000, device=DEV)
+    logits[0, 7] = 1e-3
+    logits[1] = -1e-2
+    logits[1, 9] = 0.5
+    got = mtp.mtp_token_logprobs(logits, ints([7, 9, 3]), top=1, temperature=temperature)
+    close(got.logprob, torch.tensor([0.0, 0.0, -math.log(5000)]), 2.0 ** -20)
+    close(got.entropy, torch.tensor([0.0, 0.0, math.log(5000)]), 2.0 ** -18)
+    assert got.rank.tolist() == [0, 0, 3] and got.top_ids[:, 0].tolist() == [7, 9, 0]

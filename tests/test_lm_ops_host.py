@@ -184,3 +184,12 @@ def test_kv_bound_above_the_tokens_counts_as_the_tokens(L):
         # short of the workspace, which is looked at after the sizes
         assert L.mtp_kv_attention(ctypes.byref(kv()), ctypes.byref(seqs(max_tokens=n, **ragged)), 0x80000, 1024, 128, 8, 0, 0, 0.1,
                                   0x90000, None, 0xb0000, 1000, None) == WORKSPACE
+
+
+def test_temperatures_whose_factor_leaves_the_range_are_refused(L):
+    for temperature, refused in ((3.2e-39, True), (4.1e-39, True), (4.4e-39, False), (1e-38, False)):
+        # a bad output address is looked at after the temperature
+        status = [L.mtp_token_logprobs(0x1000, 0, 1000, 3, 1000, 0x2000, temperature, 0, 0x3001, None, None, None, None, None, 0, None),
+                  L.mtp_token_logprobs_backward(0x1000, 0, 1000, 3, 1000, 0x2000, temperature, 0x4001, None, 0x4200, None, 0x5000, 1000, 0,
+                                                None)]
+        assert status == [SHAPE if refused else ALIGN] * 2
