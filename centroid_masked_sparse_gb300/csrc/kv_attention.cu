@@ -6,15 +6,16 @@
 // the 16-row operand: S^T = K Q^T, 16 tokens by 8 query rows, and O^T = V^T P^T, 16 columns
 // of the head by 8 query rows, so the heads that share a kv head and a call's query tokens
 // fill the 8 columns.  Codes become fp16 as follows:
-//  - int8: the byte c + 128, masked in place, is the fp16 subnormal (c + 128) * 2^-24; the
-//    128 * sum q (128 * sum p) leaves the sum through its start, in fp32;
+//  - int8 keys: the byte c + 128, masked in place, is the fp16 subnormal (c + 128) * 2^-24; the
+//    128 * sum q leaves the sum through its start, in fp32;
+//  - int8 values: 1152 + c, less 1152, exact.  (In the keys' way the sums would carry 128 beside
+//    each code, and a token of large weight and small values would cost the others their bits.)
 //  - e4m3: cvt to fp16, exact.
 // q, which has 8 significant bits, is fp16 times a power of two per row; p is rounded to
 // fp16's 11 bits, and the same rounded p make the denominator.  The sums of a block of 16
 // tokens start at zero and are added, times v_scale, to the row's in fp32: blocks have their
-// own scales, and sums of 128 + c would otherwise outgrow what they are to hold.  m is the
-// row's maximum so far, or up to 8 below it: p stays below 2^8, and most blocks need no
-// maximum across lanes.
+// own scales.  m is the row's maximum so far, or up to 8 below it: p stays below 2^8, and most
+// blocks need no maximum across lanes.
 //
 // Split.  A warp reads blocks of 16 tokens, two steps ahead, each lane the
 // pieces of its own operands (cp.async into its own slots: no barrier).  The CTAs of an item
@@ -63,8 +64,17 @@ template <bool INT8> __device__ __forceinline__ void key_operands(uint32_t w, ui
 template <bool INT8> __device__ __forceinline__ void value_operands(uint32_t a, uint32_t b, uint32_t (&v)[4])
 {
     const uint32_t x = __byte_perm(a, b, INT8 ? 0x5410 : 0x5140), y = __byte_perm(a, b, INT8 ? 0x7632 : 0x7362);
-    key_operands<INT8>(x, v[0], v[1]);
-    key_operands<INT8>(y, v[2], v[3]);
+    if (INT8) {
+        auto code = [](uint32_t w) {   // 1152 + c, less 1152
+            uint32_t r;
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((w & 0x00ff00ffu) ^ 0x64806480u), "r"(0x64806480u));
+            return r;
+        };
+        v[0] = code(x), v[1] = code(x >> 8), v[2] = code(y), v[3] = code(y >> 8);
+    } else {
+        key_operands<INT8>(x, v[0], v[1]);
+        key_operands<INT8>(y, v[2], v[3]);
+    }
 }
 
 // Four CTAs per SM (64 ragged sequences, D = 128: 131 us, with three and steps of eight
@@ -350,7 +360,6 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
         for (int u = 0; u < U; ++u) {
             if (!ok[u]) continue;
             uint32_t b0[NT], b1[NT];
-            float start[NT][2];
 #pragma unroll
             for (int m = 0; m < NT; ++m) {
                 float w[4];
@@ -368,10 +377,8 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
                 mma_f16_first(l, ones, ones, ones, ones, b0[m], b1[m]);
                 l_round[m][0] += l[0];
                 l_round[m][1] += l[1];
-                start[m][0] = INT8 ? l[0] * (-128.f / 16777216.f) : 0.f;
-                start[m][1] = INT8 ? l[1] * (-128.f / 16777216.f) : 0.f;
             }
-            const float scale = vs[u] * UNIT;
+            const float scale = vs[u];
             const uint8_t *values = stage + u * 32 * D + 16 * D;
 #pragma unroll
             for (int j = 0; j < (D < 128 ? 1 : D / 128); ++j) {
@@ -396,8 +403,7 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
 #pragma unroll
                         for (int m = 0; m < NT; ++m) {
                             float d[4];
-                            mma_f16_from(d, lo4[half * 2], lo4[half * 2 + 1], hi4[half * 2], hi4[half * 2 + 1], b0[m], b1[m], start[m][0],
-                                         start[m][1]);
+                            mma_f16_first(d, lo4[half * 2], lo4[half * 2 + 1], hi4[half * 2], hi4[half * 2 + 1], b0[m], b1[m]);
                             float(&acc)[4] = o[m][j * 8 + i * 2 + half];
                             fma_pair(acc[0], acc[1], scale, d[0], d[1]);
                             fma_pair(acc[2], acc[3], scale, d[2], d[3]);

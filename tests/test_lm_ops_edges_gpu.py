@@ -268,3 +268,33 @@ def test_logprobs_at_the_lowest_temperatures(temperature):
     close(got.logprob, torch.tensor([0.0, 0.0, -math.log(5000)]), 2.0 ** -20)
     close(got.entropy, torch.tensor([0.0, 0.0, math.log(5000)]), 2.0 ** -18)
     assert got.rank.tolist() == [0, 0, 3] and got.top_ids[:, 0].tolist() == [7, 9, 0]
+
+
+def one_dominant_token(g, fmt, dim, power):
+    """A cache of 32 tokens whose first one alone has keys (the others' scores are 0, and their weights 2^power of its
+    own) and no values, with the query and scale for it."""
+    cache, table = make_cache(g, [32], 1, dim, 32, fmt)
+    page = int(table[0, 0])
+    cache.k_codes[page] = 0
+    cache.k_codes[page, 0, 0, 0] = 64 if fmt == "int8" else 0x58   # 64, 16
+    cache.v_codes[page, 0, 0] = 0
+    cache.k_scales[page] = 1.0 / 64 if fmt == "int8" else 1.0 / 16
+    q = torch.zeros(1, 1, dim, dtype=BF16, device=DEV)
+    q[0, 0, 0] = 1.0
+    return cache, table, q, float(torch.tensor(-power * math.log(2)))
+
+
+def check_one_dominant_token(fmt, dim, power):
+    cache, table, q, scale = one_dominant_token(gen(33), fmt, dim, power)
+    out, lse = mtp.mtp_kv_attention(cache, table, ints([32]), q, scale=scale)
+    k, v = tokens_of(cache, table[0], 32, 0)
+    o, tol, l, ltol = one_row(q[0, 0], k, v, scale)
+    close(out[0, 0], o, tol)
+    close(lse[0, 0], l, ltol)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("power", [-12, -14, -18])
+def test_attention_values_beside_a_large_weight_without_any(fmt, dim, power):
+    check_one_dominant_token(fmt, dim, power)
