@@ -14,8 +14,9 @@
 // q, which has 8 significant bits, is fp16 times a power of two per row; p is rounded to
 // fp16's 11 bits, and the same rounded p make the denominator.  The sums of a block of 16
 // tokens start at zero and are added, times v_scale, to the row's in fp32: blocks have their
-// own scales.  m is the row's maximum so far, or up to 8 below it: p stays below 2^8, and most
-// blocks need no maximum across lanes.
+// own scales.  m is 7 below the row's maximum so far, or up to 15: p stays within 2^15, most
+// blocks need no maximum across lanes, and weights down to 2^-21 of the largest keep their 11
+// bits (those below are fp16 subnormals, off by up to 2^-32 of the largest).
 //
 // Split.  A warp reads blocks of 16 tokens, two steps ahead, each lane the
 // pieces of its own operands (cp.async into its own slots: no barrier).  The CTAs of an item
@@ -46,6 +47,7 @@ template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of 
 constexpr int kMinBlocks = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 512;
+constexpr float kHeadroom = 7.f;   // the weights' exponents above their reference
 // A cluster's sums of R rows in global memory, and their statistics once for each slice.
 constexpr int partial_floats(int D, int R) { return R * D + kMaxCluster * R * 4; }
 
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float from = top[m][e % 2] == -INFINITY ? 0.f : top[m][e % 2];   // no token of the row yet
+                    const float from = top[m][e % 2] == -INFINITY ? 0.f : top[m][e % 2] - kHeadroom;   // no token of the row yet
                     w[e] = exp2_fast(s[u][m][e] - from);
                 }
                 l_sum[m][0] += w[0] + w[2];
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(kW * 32, ctas_per_sm(D, NT)) k_kv_attention(Kv
         const int row = r0 + r;
         if (p.lse)
             p.lse[(long long)(row0 + row / share) * p.heads + h * share + row % share] =
-                e == 0.f ? -INFINITY : (most + log2f(e)) * 0.69314718055994531f;
+                e == 0.f ? -INFINITY : (most - kHeadroom + log2f(e)) * 0.69314718055994531f;
     };
     if (csize == 1 && clusters == 1) {
         __syncthreads();

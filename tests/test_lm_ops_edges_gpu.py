@@ -298,3 +298,11 @@ def check_one_dominant_token(fmt, dim, power):
 @pytest.mark.parametrize("power", [-12, -14, -18])
 def test_attention_values_beside_a_large_weight_without_any(fmt, dim, power):
     check_one_dominant_token(fmt, dim, power)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("power", [-20.5, -24, -26])
+def test_attention_small_weights_beside_a_large_one(fmt, dim, power):
+    """What the others add is all of the output, however small their weights are."""
+    check_one_dominant_token(fmt, dim, power)
