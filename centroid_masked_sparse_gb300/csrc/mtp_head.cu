@@ -74,16 +74,14 @@ cudaError_t allow_smem(const void *kernel, size_t smem)
     int dev = 0;
     cudaGetDevice(&dev);
     static std::unordered_map<FnKey, size_t, FnKeyHash> done;  // keyed by (fn, dev)
-    {
-        std::lock_guard<std::mutex> lk(g_cache_mu);
-        auto it = done.find(FnKey{kernel, dev, 0});
-        if (it != done.end() && it->second >= smem) return cudaSuccess;
-    }
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    // set and recorded under one lock: with two, a thread could set a smaller limit behind
+    // another that records a larger one
     std::lock_guard<std::mutex> lk(g_cache_mu);
-    done[FnKey{kernel, dev, 0}] = smem;
-    return cudaSuccess;
+    size_t &limit = done[FnKey{kernel, dev, 0}];
+    if (limit >= smem) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) limit = smem;
+    return e;
 }
 
 }  // namespace mtp

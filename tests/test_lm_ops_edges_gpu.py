@@ -306,3 +306,79 @@ def test_attention_values_beside_a_large_weight_without_any(fmt, dim, power):
 def test_attention_small_weights_beside_a_large_one(fmt, dim, power):
     """What the others add is all of the output, however small their weights are."""
     check_one_dominant_token(fmt, dim, power)
+
+
+_FROM_THREADS = """
+import threading, torch, centroid_masked_sparse_gb300 as mtp
+g = torch.Generator("cuda").manual_seed(1)
+widths = [256, 16384, 512, 8192, 768, 12288, 1024, 4096]
+for batch in (1, 9, 17, 25):
+    for group in (32, 64, 128):
+        weights, xs = [], []
+        for cols in widths:
+            w = (torch.randn(64, cols, device="cuda", generator=g) * 0.02).to(torch.bfloat16)
+            weights.append(mtp.Q4Weight.quantize(w, group))
+            xs.append(torch.randn(batch, cols, device="cuda", generator=g).to(torch.bfloat16))
+        torch.cuda.synchronize()
+        start, outs, errors = threading.Barrier(len(widths)), [None] * len(widths), []
+
+        def call(i):
+            try:
+                start.wait()
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    for _ in range(3):
+                        outs[i] = mtp.mtp_q4_matvec(weights[i], xs[i])
+            except Exception as e:
+                errors.append(e)
+
+        threads = [threading.Thread(target=call, args=(i,)) for i in range(len(widths))]
+        [t.start() for t in threads], [t.join() for t in threads]
+        torch.cuda.synchronize()
+        assert not errors, errors
+        for w, x, out in zip(weights, xs, outs):
+            assert torch.equal(mtp.mtp_q4_matvec(w, x), out)
+print("threads ok")
+"""
+
+
+def test_first_calls_from_several_threads():
+    """Every thread's first call of a kernel needs another amount of shared memory; later ones of each size go through."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _FROM_THREADS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert "threads ok" in run.stdout, run.stderr[-2000:]
+
+
+def test_operators_from_several_threads():
+    """Threads with a stream each, on one cache and one weight, get what a thread alone gets."""
+    import threading
+    g = gen(43)
+    cache, table = make_cache(g, [9000, 60, 4000], 2, 128, 32, "int8")
+    lengths, qs = ints([9000, 60, 4000]), [randn(g, 3, 8, 128).to(BF16) for _ in range(4)]
+    weight = mtp.Q4Weight.quantize((randn(g, 5000, 1024) * 0.1).to(BF16))
+    tokens = ints([3, 4, 5])
+
+    def step(q):
+        out, lse = mtp.mtp_kv_attention(cache, table, lengths, q)
+        logits = mtp.mtp_q4_matvec(weight, out.flatten(1))
+        scored = mtp.mtp_token_logprobs(logits, tokens, top=3)
+        return [out, lse, logits, *scored, mtp.mtp_token_logprobs_backward(logits, tokens, scored.lse, scored.entropy, scored.logprob)]
+
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def run(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got[i].append(step(qs[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(qs))]
+    [t.start() for t in threads], [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for i in range(len(qs)):
+        assert len(got[i]) == 10
+        for results in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(results, want[i]))
