@@ -74,6 +74,7 @@ class Q4Weight:
     """
 
     def __init__(self, codes, scales, zeros=None, stream=None):
+        assert codes.is_cuda, "codes must be on a GPU"
         if stream is not None:
             for t in (codes, scales, zeros):
                 if t is not None:
@@ -108,6 +109,7 @@ class Q4Weight:
 
 def mtp_q4_quantize(w, group=64, zeros=False, stream=None):
     """(codes, scales, zeros or None) of the bf16 matrix w [M, K] (unit inner stride, finite values)."""
+    assert w.is_cuda, "w must be on a GPU"
     if stream is not None:
         with torch.cuda.stream(stream):
             return mtp_q4_quantize(w, group, zeros)
@@ -157,6 +159,7 @@ class KvCache:
     """
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales, format="int8"):
+        assert k_codes.is_cuda, "the cache must be on a GPU"
         for t in (k_codes, v_codes):
             assert t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and t.shape == k_codes.shape
         for t in (k_scales, v_scales):
@@ -271,6 +274,9 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
                 cache._needs.clear()
             need = cache._needs[key] = library.mtp_kv_attention_workspace_bytes(desc, seqs, heads, max_len, window)
         workspace = cache.workspace(need)
+    else:
+        assert workspace.dtype is torch.uint8 and workspace.get_device() == where and workspace.is_contiguous(), \
+            "the workspace must be contiguous bytes on the cache's GPU"
     check(library.mtp_kv_attention(desc, seqs, q.data_ptr(), strides[0], strides[1], heads, max_len, window,
                                    dim ** -0.5 if scale is None else scale, _vector(out, torch.bfloat16, tokens * heads * dim, where),
                                    _vector(lse, torch.float32, tokens * heads, where), workspace.data_ptr(),

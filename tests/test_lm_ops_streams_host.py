@@ -106,3 +106,29 @@ def test_what_a_weight_is_made_from_is_kept_for_its_stream(notes):
     assert not OnGpu.noted
     lm_ops.Q4Weight(codes, scales, zeros, stream=Stream)
     assert {n[1:] for n in OnGpu.noted} == {(t.data_ptr(), Stream) for t in (codes, scales, zeros)}
+
+
+def test_tensors_off_the_gpu_are_refused(notes):
+    """Before anything is allocated or launched, also with a stream."""
+    bf16, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    codes, scales = torch.ones(16, 32, dtype=u8), torch.ones(16, 1, dtype=bf16)
+    for call in (lambda: lm_ops.Q4Weight(codes, scales),
+                 lambda: lm_ops.Q4Weight(codes, scales, stream=Stream),
+                 lambda: lm_ops.mtp_q4_quantize(torch.ones(16, 64, dtype=bf16)),
+                 lambda: lm_ops.Q4Weight.quantize(torch.ones(16, 64, dtype=bf16), stream=Stream),
+                 lambda: lm_ops.KvCache(*(torch.ones(4, 1, 16, 64, dtype=u8) for _ in range(2)), *(torch.ones(4, 1, dtype=f32) for _ in range(2)))):
+        with pytest.raises(AssertionError, match="on a GPU"):
+            call()
+    assert not notes
+
+
+def test_workspaces_of_another_kind_are_refused(notes):
+    cache, call = calls()["mtp_kv_attention"]
+    cache = cache()
+    notes.clear()
+    for workspace in (torch.ones(4096, dtype=torch.uint8), gpu(4096, dtype=torch.int32), gpu(64, 64, dtype=torch.uint8).t()):
+        with pytest.raises(AssertionError, match="workspace"):
+            call(cache, workspace=workspace)
+    assert all(kind == "alloc" for kind, _ in notes)
+    call(cache, workspace=gpu(4096, dtype=torch.uint8))
+    assert notes[-1] == ("launch", None)
