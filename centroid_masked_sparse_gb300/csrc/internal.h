@@ -32,8 +32,8 @@ struct DeviceScope {
     bool ok = false;
     explicit DeviceScope(int dev)
     {
-        if (cudaGetDevice(&prev) != cudaSuccess) return;
-        ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+        if (cudaGetDevice(&prev) == cudaSuccess) ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+        if (!ok) cudaGetLastError();   // the call's status says it; later launches must not read it as theirs
     }
     ~DeviceScope()
     {

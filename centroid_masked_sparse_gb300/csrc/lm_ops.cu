@@ -11,7 +11,12 @@ namespace {
 
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-mtp_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA; }
+mtp_status cuda_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return MTP_OK;
+    cudaGetLastError();   // a failed call's error is not the next one's
+    return MTP_ERR_CUDA;
+}
 
 mtp_status check_q4(int32_t rows, int32_t cols, int32_t group, int32_t device)
 {

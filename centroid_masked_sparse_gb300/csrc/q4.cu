@@ -87,6 +87,16 @@ __global__ void __launch_bounds__(256) k_q4_pack(Q4PackParams p)
     }
 }
 
+// Blocks of 256 threads; returns this launch's own status, whatever an earlier call has left.
+template <typename... KArgs, typename... Args> cudaError_t launch_plain(void (*kernel)(KArgs...), unsigned grid, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace
 
 Q4Layout q4_layout(int M, int K, int group, bool zeros)
@@ -103,8 +113,7 @@ Q4Layout q4_layout(int M, int K, int group, bool zeros)
 cudaError_t launch_q4_pack(const Q4PackParams &p, cudaStream_t s)
 {
     const long long words = (long long)p.tiles * p.blocks * 128;
-    k_q4_pack<<<(unsigned)std::min((words + 255) / 256, 32ll * sm_count()), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_plain(k_q4_pack, (unsigned)std::min((words + 255) / 256, 32ll * sm_count()), s, p);
 }
 
 template <int GROUP> cudaError_t launch_q4_group(const Q4Params &p, cudaStream_t s);   // q4_kernel.cuh
@@ -121,8 +130,7 @@ cudaError_t launch_q4_quantize(const uint16_t *w, long long ld_w, int M, int K, 
     const long long groups = (long long)M * G;
     const long long blocks = (groups + 7) / 8;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    k_q4_quantize<<<(unsigned)blocks, 256, 0, s>>>(w, ld_w, groups, G, group, codes, ld_codes, scales, zeros);
-    return cudaGetLastError();
+    return launch_plain(k_q4_quantize, (unsigned)blocks, s, w, ld_w, groups, G, group, codes, ld_codes, scales, zeros);
 }
 
 }  // namespace mtp

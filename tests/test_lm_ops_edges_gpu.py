@@ -382,3 +382,19 @@ def test_operators_from_several_threads():
         assert len(got[i]) == 10
         for results in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(results, want[i]))
+
+
+def test_a_refused_device_leaves_no_error_behind():
+    """Each call's status is its own: a call for a device that is not there, then calls that are right."""
+    import ctypes
+    from centroid_masked_sparse_gb300._lib import MtpQ4Desc, lib
+    g = gen(44)
+    w, x = (randn(g, 64, 256) * 0.1).to(BF16), randn(g, 3, 256).to(BF16)
+    weight = mtp.Q4Weight.quantize(w)
+    want, out = mtp.mtp_q4_matvec(weight, x), torch.empty(3, 64, device=DEV)
+    desc = MtpQ4Desc.from_buffer_copy(weight.desc)
+    desc.device = 99
+    for call in (lambda: mtp.mtp_q4_quantize(w), lambda: mtp.Q4Weight.quantize(w), lambda: mtp.mtp_q4_matvec(weight, x)):
+        assert lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), 256, 3, out.data_ptr(), 0, 64, None) == -5
+        call()
+    assert torch.equal(mtp.mtp_q4_matvec(mtp.Q4Weight.quantize(w), x), want)
