@@ -206,6 +206,7 @@ size_t mtp_kv_attention_workspace_bytes(const mtp_kv_desc *d, const mtp_kv_batch
     if (check_cache(d, seqs) != MTP_OK || heads < 1 || heads % d->kv_heads != 0 || max_len < 0 || window < 0) return 0;
     if (seqs->batch == 0 || seqs->tokens == 0) return MTP_KV_WORKSPACE_ZEROED;
     DeviceScope dev(d->device);   // the split depends on the device's SMs
+    if (!dev.ok && dev.prev >= 0) return 0;   // no such device (without any GPU: sizes as for one SM)
     return MTP_KV_WORKSPACE_ZEROED + kv_attention_plan(kv_params(d, seqs), heads, window, max_len).partial_floats * sizeof(float);
 }
 

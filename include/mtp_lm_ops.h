@@ -194,7 +194,8 @@ MTP_API mtp_status mtp_kv_append(const mtp_kv_desc *desc, const mtp_kv_batch *se
  *   lse      fp32 [tokens, heads] contiguous, or NULL
  *   workspace  mtp_kv_attention_workspace_bytes bytes, 16-byte aligned, whose first
  *              MTP_KV_WORKSPACE_ZEROED bytes are zero before the first call that uses it;
- *              calls leave them zero.  One call at a time, like every workspace.
+ *              calls leave them zero.  One call at a time, like every workspace.  Its size is 0
+ *              for arguments or a device that the call would refuse.
  * Scores, softmax statistics and sums are fp32; keys, values and q enter the products
  * exactly, and the weights e^(s_j - max) of the value sums with 11 significant bits, those
  * below 2^-21 to 2^-32.

@@ -398,3 +398,37 @@ def test_a_refused_device_leaves_no_error_behind():
         assert lib().mtp_q4_matvec(ctypes.byref(desc), x.data_ptr(), 256, 3, out.data_ptr(), 0, 64, None) == -5
         call()
     assert torch.equal(mtp.mtp_q4_matvec(mtp.Q4Weight.quantize(w), x), want)
+
+
+def test_workspace_of_a_device_that_is_not_there():
+    import ctypes
+    from centroid_masked_sparse_gb300._lib import MtpKvDesc, lib
+    from centroid_masked_sparse_gb300.lm_ops import _batch_desc
+    g = gen(35)
+    cache, table = make_cache(g, [50], 2, 64, 16, "int8")
+    seqs = _batch_desc(cache, table, ints([50]), None, 1, None)
+    desc = MtpKvDesc.from_buffer_copy(cache.desc)
+    desc.device = 99
+    assert lib().mtp_kv_attention_workspace_bytes(ctypes.byref(desc), ctypes.byref(seqs), 4, 0, 0) == 0
+
+
+@pytest.mark.parametrize("dim,batch,window", [(256, 1, 0), (128, 3, 0), (64, 1, 0), (256, 1, 12000)])
+def test_attention_in_a_workspace_of_its_exact_size(dim, batch, window):
+    """A split call: one byte less is refused; the size given is enough, nothing behind it is written, and its first part
+    is zero again."""
+    g = gen(dim + batch)
+    lengths = [15000 - 700 * i for i in range(batch)]
+    cache, table = make_cache(g, lengths, 1, dim, 32, "int8")
+    q = randn(g, batch, 4, dim).to(BF16)
+    want = mtp.mtp_kv_attention(cache, table, ints(lengths), q, window=window)
+    need = mtp.mtp_kv_attention_workspace_bytes(cache, table, ints(lengths), batch, 4, window=window)
+    assert need > mtp.MTP_KV_WORKSPACE_ZEROED and need % 4 == 0
+    room = torch.full((need + 65536,), 0xa5, dtype=torch.uint8, device=DEV)
+    room[:mtp.MTP_KV_WORKSPACE_ZEROED] = 0
+    with pytest.raises(mtp.MtpError):
+        mtp.mtp_kv_attention(cache, table, ints(lengths), q, window=window, workspace=room[:need - 1])
+    for _ in range(3):
+        got = mtp.mtp_kv_attention(cache, table, ints(lengths), q, window=window, workspace=room[:need])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert (room[:mtp.MTP_KV_WORKSPACE_ZEROED] == 0).all() and (room[need:] == 0xa5).all()
+    assert not (room[mtp.MTP_KV_WORKSPACE_ZEROED:need] == 0xa5).all()
