@@ -211,6 +211,13 @@ class KvCache:
         return bits
 
 
+def _token_strides(t, tokens, heads):
+    """Strides of tokens and heads, 0 where there is one: tensors carry any number there."""
+    token, head, inner = t.stride()
+    assert inner == 1
+    return token if tokens > 1 else 0, head if heads > 1 else 0
+
+
 def _batch_desc(cache, page_table, lengths, starts, tokens, max_tokens):
     batch, width = page_table.shape
     where, strides = cache.where, page_table.stride()
@@ -232,8 +239,7 @@ def mtp_kv_append(cache, page_table, lengths, k, v, starts=None, max_new=None, s
     tokens, heads, dim = shape
     assert heads == cache.kv_heads and dim == cache.head_dim and v.shape == shape
     assert k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.get_device() == where and v.get_device() == where
-    k_strides, v_strides = k.stride(), v.stride()
-    assert k_strides[2] == 1 and v_strides[2] == 1
+    k_strides, v_strides = _token_strides(k, tokens, heads), _token_strides(v, tokens, heads)
     seqs = _batch_desc(cache, page_table, lengths, starts, tokens, max_new)
     check(lib().mtp_kv_append(cache.desc, seqs, k.data_ptr(), k_strides[0], k_strides[1],
                               v.data_ptr(), v_strides[0], v_strides[1], _stream(stream, cache.index)), "mtp_kv_append")
@@ -256,8 +262,8 @@ def mtp_kv_attention(cache, page_table, lengths, q, starts=None, max_q=None, max
             return mtp_kv_attention(cache, page_table, lengths, q, starts, max_q, max_len, window, scale, out, lse, workspace)
     shape, where = q.shape, cache.where
     tokens, heads, dim = shape
-    strides = q.stride()
-    assert q.dtype is torch.bfloat16 and dim == cache.head_dim and strides[2] == 1 and q.get_device() == where
+    strides = _token_strides(q, tokens, heads)
+    assert q.dtype is torch.bfloat16 and dim == cache.head_dim and q.get_device() == where
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
     if lse is None:

@@ -432,3 +432,18 @@ def test_attention_in_a_workspace_of_its_exact_size(dim, batch, window):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert (room[:mtp.MTP_KV_WORKSPACE_ZEROED] == 0).all() and (room[need:] == 0xa5).all()
     assert not (room[mtp.MTP_KV_WORKSPACE_ZEROED:need] == 0xa5).all()
+
+
+def test_strides_of_one_token_or_head_do_not_matter():
+    g = gen(36)
+    cache, table = make_cache(g, [50], 1, 64, 16, "int8")
+    wide = randn(g, 1, 68).to(BF16)
+    q = wide[:, :64].unsqueeze(1)
+    assert q.shape == (1, 1, 64) and q.stride(0) % 8
+    want = mtp.mtp_kv_attention(cache, table, ints([50]), q.reshape(64).clone().view(1, 1, 64))
+    got = mtp.mtp_kv_attention(cache, table, ints([50]), q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    new = [mtp.KvCache.allocate(4, 16, 1, 64, "int8") for _ in range(2)]
+    for c, x in zip(new, (q, q.reshape(64).clone().view(1, 1, 64))):
+        mtp.mtp_kv_append(c, ints([[0, 1]]), ints([3]), x, x)
+    assert torch.equal(new[0].k_codes, new[1].k_codes) and torch.equal(new[0].v_scales, new[1].v_scales)
