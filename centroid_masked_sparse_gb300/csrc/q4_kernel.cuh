@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     constexpr int SG = kCols / GROUP;      // groups of a step
     constexpr int STAGE = kStage<GROUP, ZEROS, TILES>, SCALES = kScales<GROUP>, ZPS = kZeros<GROUP>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_factor[NT * 8], s_inverse[NT * 8];
+    __shared__ float s_factor[NT * 8];
+    __shared__ float2 s_inverse[NT * 8];   // its inverse times 2^24, as two factors that keep sums within fp32's range
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int b0 = blockIdx.y * NT * 8;
     const uint8_t *ring = smem + warp * S * STAGE;
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
         if (lane == 0) {
             s_factor[n] = f;
             // a row that holds a NaN or an infinity gives NaN
-            s_inverse[n] = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fp16_factor_inverse(e);
+            const float inverse = top >= 0x7f80u ? __uint_as_float(0x7fffffffu) : fp16_factor_inverse(e);
+            s_inverse[n] = inverse < 1.f ? make_float2(inverse * 16777216.f, 1.f) : make_float2(16777216.f, inverse);
         }
         __syncwarp();
         put_x(u, n, 0, words_of(0), f);
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
 
     auto store = [&](float y, int m, int n) {
         if (m >= p.M || b0 + n >= p.B) return;
-        y = y * 16777216.f * s_inverse[n];
+        y = y * s_inverse[n].x * s_inverse[n].y;
         if (p.softcap > 0.f) y = p.softcap * tanhf(y / p.softcap);
         if (p.bf16_out)
             ((uint16_t *)p.out)[(b0 + n) * p.ld_out + m] = bf16_bits(y);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
 // Columns of x that fit beside the rings of W warps of S slots.
 template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> constexpr int q4_room()
 {
-    constexpr long long left = 227 * 1024 - NT * 64 - (long long)W * S * kStage<GROUP, ZEROS, TILES>;
+    constexpr long long left = 227 * 1024 - NT * 96 - (long long)W * S * kStage<GROUP, ZEROS, TILES>;
     static_assert(left >= NT * 544 * kCols / 32, "a step of x fits");
     static_assert(TILES == 2 || S * kStage<GROUP, ZEROS, TILES> >= 2 * NT * 512, "the warps' sums fit the rings");
     return (int)(left / (NT * 544) * 32 / kCols * kCols);   // 512 + 32 bytes per 32 columns and 8 rows

@@ -447,3 +447,19 @@ def test_strides_of_one_token_or_head_do_not_matter():
     for c, x in zip(new, (q, q.reshape(64).clone().view(1, 1, 64))):
         mtp.mtp_kv_append(c, ints([[0, 1]]), ints([3]), x, x)
     assert torch.equal(new[0].k_codes, new[1].k_codes) and torch.equal(new[0].v_scales, new[1].v_scales)
+
+
+def test_q4_large_scales_and_small_inputs():
+    """Scales and inputs whose products are of ordinary size although neither is."""
+    g = gen(38)
+    codes, scales, points = q4_weight(g, 64, 1024, 64, True)
+    x = randn(g, 4, 1024).to(BF16)
+    scales[3], scales[4] = 1e35, 1e30
+    x[1] *= 2.0 ** -80
+    x[2] *= 2.0 ** -110
+    x[3] *= 2.0 ** 100
+    want, tol = ref.q4_matvec(codes, scales, points, 64, x, 0.0, False)
+    fits = want.abs() < 1e38
+    fits[:, 3] = fits[:, 4] = False
+    fits[1:3, 3] = fits[1:3, 4] = True
+    close(mtp.mtp_q4_matvec(mtp.Q4Weight(codes, scales, points), x).cpu()[fits], want[fits], (tol + 1e-38)[fits])
