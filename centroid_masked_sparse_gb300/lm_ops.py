@@ -205,9 +205,12 @@ class KvCache:
         return ws
 
     def read_errors(self):
-        """The MTP_DEVERR_* bits that the calls so far have set (waits for the GPU), and clears them."""
+        """The MTP_DEVERR_* bits that the calls so far have set, on any stream (waits for the GPU), and clears them."""
+        torch.cuda.synchronize(self.device)
         bits = int(self.errors.item())
-        self.errors.zero_()
+        if bits:
+            self.errors.zero_()
+            torch.cuda.synchronize(self.device)   # before a call on another stream sets new ones
         return bits
 
 

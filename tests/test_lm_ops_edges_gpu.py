@@ -463,3 +463,19 @@ def test_q4_large_scales_and_small_inputs():
     fits[:, 3] = fits[:, 4] = False
     fits[1:3, 3] = fits[1:3, 4] = True
     close(mtp.mtp_q4_matvec(mtp.Q4Weight(codes, scales, points), x).cpu()[fits], want[fits], (tol + 1e-38)[fits])
+
+
+def test_errors_of_calls_on_other_streams():
+    """read_errors waits for every stream, and what it clears is cleared before later calls on any."""
+    g = gen(45)
+    cache, table = make_cache(g, [50], 1, 64, 16, "int8")
+    q, bad, lengths, side = randn(g, 1, 2, 64).to(BF16), torch.full_like(table, -1), ints([50]), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            mtp.mtp_kv_attention(cache, bad, lengths, q)
+        assert cache.read_errors() == mtp.MTP_DEVERR_PAGE
+        mtp.mtp_kv_attention(cache, bad, lengths, q, stream=side)
+        assert cache.read_errors() == mtp.MTP_DEVERR_PAGE
+        assert cache.read_errors() == 0
