@@ -199,7 +199,8 @@ MTP_API mtp_status mtp_kv_append(const mtp_kv_desc *desc, const mtp_kv_batch *se
  * Scores, softmax statistics and sums are fp32; keys, values and q enter the products
  * exactly, and the weights e^(s_j - max) of the value sums with 11 significant bits, those
  * below 2^-21 to 2^-32.
- * Non-finite q, scales or e4m3 codes give what IEEE arithmetic gives. */
+ * Non-finite q, scales or e4m3 codes give what IEEE arithmetic gives (an infinite scale of
+ * values that not every query of a sequence sees: NaN), in the queries that see them only. */
 #define MTP_KV_WORKSPACE_ZEROED 262144u
 MTP_API size_t mtp_kv_attention_workspace_bytes(const mtp_kv_desc *desc, const mtp_kv_batch *seqs, int32_t heads,
                                                 int32_t max_len, int32_t window);

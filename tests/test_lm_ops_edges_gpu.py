@@ -479,3 +479,43 @@ def test_errors_of_calls_on_other_streams():
         mtp.mtp_kv_attention(cache, bad, lengths, q, stream=side)
         assert cache.read_errors() == mtp.MTP_DEVERR_PAGE
         assert cache.read_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("share", [1, 3])
+@pytest.mark.parametrize("length,window,bad", [(40, 0, "token 38"), (34, 0, "page 2"), (18, 2, "page 0"), (18, 2, "page 1"), (300, 0, "token 297"),
+                                              (38, 3, "token 33")])
+def test_attention_non_finite_values_that_a_query_does_not_see(fmt, dim, share, length, window, bad):
+    """Five query tokens, some of which see a token with NaN codes or a page with a NaN or infinite scale: the others'
+    outputs are what they would be without."""
+    g = gen(length + dim)
+    cache, table = make_cache(g, [length], 1, dim, 16, fmt)
+    q = randn(g, 5, share, dim).to(BF16)
+    scale = dim ** -0.5
+    what, at = bad.split()
+    at = int(at)
+    if what == "token":
+        if fmt == "int8":
+            pytest.skip("int8 codes are all finite")
+        cache.v_codes[int(table[0, at // 16]), 0, at % 16, ::3] = 0x7f
+        cache.k_codes[int(table[0, at // 16]), 0, at % 16, 5] = 0xff
+        spoilt = {at}
+    else:
+        cache.v_scales[int(table[0, at])] = math.nan if share == 1 else math.inf
+        spoilt = set(range(at * 16, at * 16 + 16))
+    out, lse = mtp.mtp_kv_attention(cache, table, ints([length]), q, window=window)
+    seen_by_none = True
+    for i in range(5):
+        p = length - 5 + i
+        low = max(0, p - window + 1) if window else 0
+        if spoilt & set(range(low, p + 1)):
+            assert not torch.isfinite(out[i]).all()
+            continue
+        seen_by_none = False
+        for h in range(share):
+            k, v = tokens_of(cache, table[0], length, 0)
+            o, tol, l, ltol = one_row(q[i, h], k[low:p + 1], v[low:p + 1], scale)
+            close(out[i, h], o, tol)
+            close(lse[i, h], l, ltol)
+    assert not seen_by_none
