@@ -519,3 +519,59 @@ def test_attention_non_finite_values_that_a_query_does_not_see(fmt, dim, share, 
             close(out[i, h], o, tol)
             close(lse[i, h], l, ltol)
     assert not seen_by_none
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim,heads", [(64, 3), (128, 12), (256, 4)])
+@pytest.mark.parametrize("lengths,counts,window", [
+    ([20000], [1], 0), ([20000], [4], 0), ([9001, 15003], [3, 1], 0), ([20000], [1], 12345), ([18011, 300], [4, 2], 9000),
+])
+def test_attention_joined_from_several_clusters(fmt, dim, heads, lengths, counts, window):
+    """Items of more than one cluster, whose sums go through global memory: each head size, with and without a window
+    that spans several of them."""
+    from tests.test_lm_ops_gpu import check_attention
+    g = gen(sum(lengths) + dim)
+    cache, table = make_cache(g, lengths, 1, dim, 64, fmt)
+    q = randn(g, sum(counts), heads, dim).to(BF16)
+    starts = [0]
+    for n in counts:
+        starts.append(starts[-1] + n)
+    need = mtp.mtp_kv_attention_workspace_bytes(cache, table, ints(lengths), sum(counts), heads, starts=ints(starts), max_q=max(counts),
+                                                window=window)
+    assert need > mtp.MTP_KV_WORKSPACE_ZEROED   # more than one cluster
+    out, lse = check_attention(cache, table, lengths, counts, q, window=window)
+    again = mtp.mtp_kv_attention(cache, table, ints(lengths), q, starts=ints(starts), max_q=max(counts), window=window)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dim,fmt", [(64, "int8"), (128, "e4m3"), (256, "int8")])
+def test_attention_of_a_prompt(dim, fmt):
+    """More query tokens than a tile holds rows, one prompt from its first token and one behind cached ones."""
+    from tests.test_lm_ops_gpu import check_attention
+    g = gen(dim)
+    lengths, counts = [130, 300], [130, 77]
+    cache, table = make_cache(g, lengths, 2, dim, 32, fmt)
+    check_attention(cache, table, lengths, counts, randn(g, 207, 6, dim).to(BF16))
+    check_attention(cache, table, lengths, counts, randn(g, 207, 6, dim).to(BF16), window=50)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_of_a_prompt_with_a_head_of_256(fmt):
+    g = gen(46)
+    befores, counts = [37, 0], [700, 1030]
+    cache, table = make_cache(g, [b + n for b, n in zip(befores, counts)], 2, 256, 64, fmt)
+    k, v = (randn(g, 1730, 2, 256).to(BF16) for _ in range(2))
+    want = [ref.append(codes, scales, fmt, table, befores, [0, 700, 1730], x)
+            for codes, scales, x in ((cache.k_codes, cache.k_scales, k), (cache.v_codes, cache.v_scales, v))]
+    mtp.mtp_kv_append(cache, table, ints(befores), k, v, starts=ints([0, 700, 1730]), max_new=1030)
+    for got, (codes, scales) in zip(((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)), want):
+        assert torch.equal(got[1].cpu(), scales) and torch.equal(got[0].cpu(), codes)
+
+
+@pytest.mark.parametrize("rows,cols,batch", [(3000, 1024, 512), (257, 4096, 1024), (40000, 512, 200)])
+def test_q4_of_a_prompt(rows, cols, batch):
+    g = gen(rows)
+    codes, scales, points = q4_weight(g, rows, cols, 64, True)
+    x = randn(g, batch, cols).to(BF16)
+    want, tol = ref.q4_matvec(codes, scales, points, 64, x, 0.0, True)
+    close(mtp.mtp_q4_matvec(mtp.Q4Weight(codes, scales, points), x, out_dtype=BF16), want, tol)
