@@ -582,25 +582,54 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
 // but the type's lowest value, all of ln V is gone), so one CTA reads the row once more for its
 // maximum m and l = ln sum e^((x - m) factor), and writes all of it.  ln p is held at kNoWeight
 // from below, where p is 0, so that masked tokens and 0 * -inf need no branch.  Bound by HBM:
-// 1024 rows of 262144 bf16 take 159 us, 99 % of a copy's rate; 61 rows of 32003 6.6 us, the time
-// of the host's call.
+// 1024 rows of 262144 bf16 take 156.4 us, 101 % of a copy's rate; 61 rows of 50021 fp32 3.6 us.
+// Read once more they take 350 and 15 us (reading a logit at a time 440 and 17).
 constexpr int kGradVecs = 4;   // vectors of a thread
 constexpr float kExactLse = 1024.f, kNoWeight = -1024.f;
 
-// The row's largest logit and the logarithm of its sum, for every thread of the CTA.
-template <bool BF16> __device__ __noinline__ float2 largest_and_sum(const typename Logits<BF16>::type *x, int vocab, float factor)
+// The row's largest logit and the logarithm of its sum, for every thread of the CTA.  The row is
+// `head` scalars, `vecs` vectors and scalars.
+template <bool BF16>
+__device__ __forceinline__ float2 largest_and_sum(const typename Logits<BF16>::type *x, int vocab, int head, int vecs, float factor)
 {
+    typedef Logits<BF16> L;
     __shared__ float s_most[kGradThreads / 32], s_sum[kGradThreads / 32];
     const float c = factor * kLog2e;
+    const uint4 *base = (const uint4 *)(x + head);
+    constexpr int N = 2;   // vectors at a time: more need more registers, and the common rows want six CTAs per SM
+    const uint4 masked = make_uint4(L::masked(), L::masked(), L::masked(), L::masked());
     float most = -INFINITY, sum = 0.f;
-    for (int i = threadIdx.x; i < vocab; i += kGradThreads) {
-        const float v = Logits<BF16>::value(x[i]);
-        if (v > most) {
-            sum *= exp2_fast((most - v) * c);   // 0 for the first
-            most = v;
-        }
-        sum += v == -INFINITY ? 0.f : exp2_fast((v - most) * c);
+    auto raise = [&](float to) {
+        if (!(to > most)) return;
+        sum *= exp2_fast((most - to) * c);   // 0 for the first
+        most = to;
+    };
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += N * kGradThreads) {
+        uint4 v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = i0 + j * kGradThreads < vecs ? base[i0 + j * kGradThreads] : masked;
+        float high = -INFINITY, part[N] = {};
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < L::VEC; ++e) high = fmaxf(high, element<BF16>(v[j], e));
+        raise(high);
+        const float from = most == -INFINITY ? 0.f : most;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < L::VEC; ++e) part[j] += exp2_fast((element<BF16>(v[j], e) - from) * c);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum += part[j];
     }
+    auto one = [&](int i) {
+        const float v = L::value(x[i]);
+        raise(v);
+        sum += v == -INFINITY ? 0.f : exp2_fast((v - most) * c);
+    };
+    if (threadIdx.x < head) one(threadIdx.x);
+    if (threadIdx.x < vocab - head - vecs * L::VEC) one(head + vecs * L::VEC + threadIdx.x);
     auto join = [&](float m, float s) {
         const float up = fmaxf(most, m);
         sum = (most == up ? sum : sum * exp2_fast((most - up) * c)) + (m == up ? s : s * exp2_fast((m - up) * c));
@@ -614,7 +643,7 @@ template <bool BF16> __device__ __noinline__ float2 largest_and_sum(const typena
     return make_float2(most, logf(sum));
 }
 
-template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_logprobs_backward(LogprobGradParams p)
+template <bool BF16> __global__ void __launch_bounds__(kGradThreads, 6) k_token_logprobs_backward(LogprobGradParams p)
 {
     typedef Logits<BF16> L;
     typedef typename L::type T;
@@ -641,8 +670,9 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads) k_token_log
     float most = 0.f, lse = lse_in == -INFINITY ? 0.f : lse_in;   // nothing but masked tokens: all 0
     if (far) {
         if (blockIdx.y > 0) return;
-        const float2 exact = largest_and_sum<BF16>(x, p.vocab, p.factor);   // every read is before the first write
+        const float2 exact = largest_and_sum<BF16>(x, p.vocab, head, vecs, p.factor);   // every read is before the first write
         most = exact.x, lse = exact.y;
+        load(0);   // again: the first need not stay in registers meanwhile
     }
     const int stride = far ? each : gridDim.y * each;
     const int given = p.tokens ? __ldg(p.tokens + row) : -1;
