@@ -25,11 +25,12 @@
 // head's columns.  Only an item with more than one cluster goes through global memory: the
 // last cluster to arrive, per slice, adds the others' sums in their order.
 //
-// What bounds it: latency.  64 ragged sequences of up to 8191 tokens (8 kv heads of 128, 617
-// MB) take 131 us, 4.7 TB/s, with instructions in 0.44 of the issue slots and the tensor pipe
-// 13 % busy.  One sequence of 65519 tokens (one kv head of 256, 33.6 MB) takes 16.8 us: its
+// What bounds it: latency, and the ends of unequal CTAs.  64 ragged sequences of up to 8191
+// tokens (8 kv heads of 128, 617 MB) take 127.6 us, 4.8 TB/s, with instructions in 0.46 of the
+// issue slots and the tensor pipe 13 % busy: every item gets the same number of CTAs, whatever
+// its length.  One sequence of 65519 tokens (one kv head of 256, 33.6 MB) takes 16.4 us: its
 // chain of look-ups, few steps and joins.  16 sequences of up to five query tokens in a window
-// of 512 take 12.7 us, one pass through that chain.  A warp per query row on the CUDA cores took
+// of 512 take 12.6 us, one pass through that chain.  A warp per query row on the CUDA cores took
 // 20.8 ms, 3 ms and 138 us.
 #include <algorithm>
 
@@ -41,9 +42,9 @@ namespace {
 
 constexpr int kW = 4;            // warps of a CTA
 template <int D> constexpr int kStageOf = D == 256 ? 8192 : 4096;   // bytes of codes of a step
-// Blocks of 16 tokens that a CTA should have at least (65519 tokens, D = 256: 128, 192, 256, 304,
-// 384 CTAs 24, 20.4, 17.1, 20.3, 18.8 us; 8191 tokens, 8 kv heads of 128: 16 blocks 10.6 us,
-// eight 11.5, 24 12).
+// Blocks of 16 tokens that a CTA should have at least (65519 tokens, D = 256: 17.2 us, with eight
+// 25.6, with 24 20.9; 16 sequences of 8 tokens, a window of 1024 and 8 kv heads of 128: 34.6, 34.6
+// and 31.8).
 constexpr int kMinBlocks = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSplits = 512;
@@ -79,8 +80,8 @@ template <bool INT8> __device__ __forceinline__ void value_operands(uint32_t a, 
     }
 }
 
-// Four CTAs per SM (64 ragged sequences, D = 128: 131 us, with three and steps of eight
-// kilobytes 136) where their sums leave the registers for it.
+// Four CTAs per SM (64 ragged sequences, D = 128, with the zeroing of a graph's workspace: 128.8
+// us, with three and steps of eight kilobytes 137.9) where their sums leave the registers for it.
 constexpr int ctas_per_sm(int D, int NT) { return NT > 1 ? 2 : D > 128 ? 3 : 4; }
 // The rings of a CTA's warps, or the sums that take their place.
 constexpr int ring_bytes(int D, int NT)
@@ -706,11 +707,11 @@ KvAttentionPlan kv_attention_plan(const KvParams &c, int heads, int window, int 
     // the 3 % that whole clusters leave empty, or four rounds where even one each is half of
     // that.  Unlike ones: one cluster each, in up to four rounds, or more clusters where a round
     // and a quarter has room (32 heads on 8, D = 128, up to 8191 tokens: 8 sequences with 4, 8,
-    // 16, 24 CTAs an item 33, 24, 29, 29 us; 24 sequences with 2, 4, 8, 16: 70, 63, 59, 73 us; 4
-    // sequences with 8, 16, 24, 32: 18, 15.6, 14.8, 15.3 us; the window of 512, 64 items, with 2,
-    // 4, 8: 13.8, 12.8, 18.8 us).  At D = 256, whose joins are larger, clusters of four where
-    // these fill two thirds of the places (80 items of up to 4434 tokens with 2, 4, 8: 50, 40, 45
-    // us; 37 items of up to 5889 with 4, 8, 16: 36, 28, 33 us).
+    // 16, 24 CTAs an item 32.5, 24.4, 29.5, 28.5 us; 24 sequences with 2, 4, 8, 16: 69, 61, 59, 73
+    // us; 4 sequences with 8, 16, 24, 32: 16.6, 14.4, 14.3, 14.4 us; the window of 512, 64 items,
+    // with 2, 4, 8: 13.9, 12.7, 18.6 us).  At D = 256, whose joins are larger, clusters of four
+    // where these fill two thirds of the places (80 items of up to 4434 tokens with 2, 4, 8: 53,
+    // 38, 41 us; 37 items of up to 5889 with 4, 8, 16: 37, 27, 31 us).
     const bool alike = c.batch == 1 || window > 0;
     const long long fit = slots * 97 / 100 / plan.items, loose = slots * 5 / 4 / plan.items, rounds = 4 * slots / plan.items;
     const long long one = c.dim == 256 && plan.items * 6 >= slots ? 4 : 8;

@@ -157,7 +157,6 @@ mtp_status mtp_q4_matvec(const mtp_q4_desc *d, const void *x, int64_t ld_x, int3
     p.M = d->rows;
     p.K = d->cols;
     p.group = d->group;
-    p.G = d->cols / d->group;
     p.blocks = (d->cols + 63) / 64;
     p.B = batch;
     p.bf16_out = out_type == MTP_TYPE_BF16;

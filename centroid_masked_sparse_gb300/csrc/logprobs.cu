@@ -17,10 +17,13 @@
 // them all (ties by the thousand), all vectors are read again in rounds that it holds, with
 // sorted lists of 32 a warp between them.
 //
-// What bounds it: HBM for fp32; for bf16 instructions, 13 for two logits, although sums and
-// comparisons work on packed pairs: 320 rows of 262144 take 41.7 us with 20 alternatives, 4.0
-// TB/s, and 33.8 with none; in fp32 59 us, 5.7 TB/s.  One row takes 9 us, all
-// latency: a third of it its own reading, the rest the search and the joins of eight CTAs.
+// What bounds it: HBM for fp32; for bf16 neither that nor the issue slots alone.  320 rows of
+// 262144 take 41.9 us with 20 alternatives, 4.0 TB/s, and 33.9 with none, 5 TB/s; two logits
+// take 21.4 and 17.5 instructions (13 of them the sums, the maximum and the rank, on packed
+// pairs), which fill 0.62 of the slots; what is missing is loads in flight, at 24 warps per SM
+// and, for 8 us, searches beside which a CTA reads next to nothing.  In fp32 60 us, 5.6 TB/s.
+// One row takes 9.2 us, all latency: a third of it its own reading, the rest the search and the
+// joins of eight CTAs.
 #include <algorithm>
 #include <type_traits>
 
@@ -741,18 +744,18 @@ template <bool BF16> __global__ void __launch_bounds__(kGradThreads, 6) k_token_
 template <bool BF16, bool TOP, int W> cudaError_t launch_logprobs(const LogprobParams &p, cudaStream_t s)
 {
     // CTAs of a row: as many as are resident at once for all rows, of two tiles each at least.
-    // Clusters do not fit the last 15 % of the places, and a second wave costs more (100 rows in
-    // fp32: 25 us with four CTAs, 37 with six; 320 rows in bf16: 43 with three, 46 with two)
-    // (launches one after the other; 64 rows in fp32: 22 us with eight, 24 with four; one
-    // row: 12.5 with eight, 14.5 with sixteen)
+    // Clusters do not fit the last 15 % of the places, and a second wave costs more (rows of
+    // 262144 with 20 alternatives; 100 in fp32: 24.3 us with four CTAs, 35.1 with six; 320 in
+    // bf16: 42.2 with three, 43.9 with two, 45.0 with four; 64 in fp32: 19.7 with eight, 20.3
+    // with four; one masked row: 9.4 with eight, 11.2 with four)
     const long long tile = W * 32 * kVecs * (BF16 ? 8 : 4), slots = 32ll / W * sm_count();
     const int cluster = (int)std::max(1ll, std::min({8ll, slots * 85 / 100 / p.rows, p.vocab / (2 * tile)}));
     return launch_clusters(k_token_logprobs<BF16, TOP, W>, dim3((unsigned)p.rows * cluster), dim3(W * 32), cluster, 0, s, p);
 }
 
 // Many rows: CTAs of four warps, whose searches for alternatives hold up less (2000 rows of
-// 32003 bf16: 39 us, with eight warps 47; 320 of 262144: 46 and 47).  Few: eight (64 rows of
-// 262144 fp32: 20 us, with four warps 22.5; one row: 10.6 and 12.6).
+// 32003 bf16: 40.8 us, with eight warps 49.4; 320 of 262144: 42.0 and 47.6).  Few: eight (64
+// rows of 262144 fp32: 19.7 us, with four warps 21.1; one row: 9.4 and 11.1).
 template <bool BF16, bool TOP> cudaError_t launch_logprobs_rows(const LogprobParams &p, cudaStream_t s)
 {
     return p.rows > 2 * sm_count() ? launch_logprobs<BF16, TOP, 4>(p, s) : launch_logprobs<BF16, TOP, 8>(p, s);

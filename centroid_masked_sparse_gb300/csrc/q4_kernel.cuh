@@ -14,12 +14,13 @@
 //  - the zero point leaves the sum as -z * sum_k x[b, k] of the group, in fp32.  Its
 //    magnitude is about that of the sum (codes lie in 0..15), so the difference loses about
 //    one bit of fp32's 24.
-// Both, times the group's scale, are added to the row's sum in fp32.
+// Both, times the group's scale, are added to the row's sum in fp32.  (262144 x 1536 with 8
+// rows ends 4.6e-7 of the outputs' size off in the mean, products in fp32 alone 1.3e-7.)
 //
 // What bounds it.  HBM up to 8 batch rows: 4.25 bits a weight with groups of 64; 262144 x
-// 1536 with 8 rows takes 39.3 us behind another launch, 5.7 TB/s, the same loads and stores
-// without the products about 2 us less.  Above, the products and what feeds them: 51.5 us at
-// 16 rows, 82.6 at 32; 50021 x 2592 with 23 rows takes 38 us with the tensor pipe 35 % busy,
+// 1536 with 8 rows takes 39.1 us behind another launch, 5.7 TB/s, the same loads and stores
+// without the products about 2 us less.  Above, the products and what feeds them: 50 us at
+// 16 rows, 83 at 32; 50021 x 2592 with 23 rows takes 38 us with the tensor pipe 35 % busy,
 // one round of tiles a warp and x in two chunks.  Unpacking to bf16 with a subtraction of the
 // zero point took 23 integer instructions for every 8 here (61 us at 8 rows).
 #pragma once
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(W * 32, 1) k_q4_matvec(Q4Params p, Q4Plan plan
     // and chunks.  With TILES = 1 the CTA has at most a tile for each warp.  Up to 16 batch rows
     // (TWO) each chunk's steps of all tiles, one tile after the other, are shared evenly: a warp
     // has steps of tile t0 (of the CTA's) and perhaps of the next (21488 x 3392, 9 tiles a CTA, 5
-    // rows: 13 us, 17 with a tile for each warp).  Above, where a second tile's
+    // rows: 10.5 us, 11.8 with a power of two of warps for each tile).  Above, where a second tile's
     // sums would not stay in registers (2048 x 4096, 32 rows: 16.5 us, without 14.8), `parts`
     // warps share each tile's steps.
     constexpr bool SPREAD = TILES == 1, TWO = SPREAD && NT <= 2;
@@ -375,12 +376,13 @@ template <int NT, int GROUP, bool ZEROS, int W, int S, int TILES> cudaError_t la
 }
 
 // 12 warps of two tiles where a CTA has more than 16 tiles, else 16 of one, which compute no
-// tile that is not there (8192 x 4096, 32 rows: 21.5 us, with 8 warps of two 29.4; 16384 x
-// 4096, one row: 10.6 and 15.2; 38000 x 2048, 8 rows, 16 tiles a CTA: 11.0 and 10.8).  Launches one
-// after the other: 262144 x 1536, 8 rows: 12 warps 43.3, 16 warps of two 45.5 us; 50021 x 2592,
-// 23 rows: 43 with 12, 55 with 8, 53 with 16.  Three slots if x fits beside them (262144 x
-// 1536, 8 rows: 45.3 with two).  With x in chunks 8 warps are ahead up to 8 batch rows (65536 x
-// 8192: 70 against 93 us), 12 above (90000 x 4096, 32 rows: 111 against 123).
+// tile that is not there (8192 x 4096, 32 rows: 21.4 us, with 8 warps of two 39.4; 16384 x
+// 4096, one row: 9.7 and 15.0; 38000 x 2048, 8 rows, 16 tiles a CTA: 9.8, with 12 warps of two
+// 11.1).  262144 x 1536, 8 rows: 12 warps 39.2, 16 warps of two 41.2 us; 50021 x 2592, 23 rows:
+// 37.8 with 12, 55.9 with 8, 49.0 with 16.  Three slots if x fits beside them (262144 x 1536, 8
+// rows: 40.8 with two; at 16 rows two would be ahead, 48.8 against 50.0).  With x in chunks 8
+// warps are ahead up to 8 batch rows (65536 x 8192: 64.8 against 85.8 us), 12 above (90000 x
+// 4096, 32 rows: 104.8 against 122.6).
 template <int NT, int GROUP, bool ZEROS> cudaError_t launch_q4(const Q4Params &p, cudaStream_t s)
 {
     Q4Plan plan{};
