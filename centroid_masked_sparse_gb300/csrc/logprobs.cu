@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(W * 32, 32 / W) k_token_logprobs(LogprobParams
 }
 
 // grad_i = factor * (g_l (i == given) - p_i (g_l + g_e (ln p_i + h))), ln p_i = (x_i - m) factor - l.
-// m and l are 0 and lse, whose rounding is at most 2^-24 |lse| of p, where that stays below
+// m and l are 0 and lse, whose roundings make at most 2^-22 |lse| of p, where that stays below
 // kExactLse.  Beyond, fp32 has no room for l beside x factor (at -1e9, or with a row of nothing
 // but the type's lowest value, all of ln V is gone), so one CTA reads the row once more for its
 // maximum m and l = ln sum e^((x - m) factor), and writes all of it.  ln p is held at kNoWeight

@@ -242,8 +242,8 @@ MTP_API mtp_status mtp_token_logprobs(const void *logits, int32_t type, int64_t 
  *   grad_logits[r, i] = (g_l * ((i == token) - p_i) - g_e * p_i * (ln p_i + entropy[r])) / temperature
  * with g_l taken as 0 for a row without a given token; masked tokens get 0.
  *   lse, entropy   of the forward call (entropy is read only with grad_entropy).  p has a
- *                relative error of up to 2^-24 |lse| from lse's own rounding; a row of |lse| >=
- *                1024 is summed again instead
+ *                relative error of up to 2^-22 |lse| from lse's own roundings; a row of |lse| >=
+ *                1024 is summed again instead.  A p below 2^-126 counts as 0
  *   grad_logprob, grad_entropy   fp32 [rows]; either may be NULL, not both; tokens may be
  *                NULL without grad_logprob
  *   grad_logits  [rows, ld_grad] of the logits' type; may be the logits themselves (same
